@@ -158,8 +158,9 @@ def _x8_codes(x, dtype):
     v = _groups(x.float(), 32)
     fine = torch.isfinite(v)
     kept = torch.where(fine, v, torch.zeros_like(v)).clamp(-X8_LIMIT[dtype], X8_LIMIT[dtype])
-    fraction, power = torch.frexp(kept.abs().amax(2))
-    e = (power - 9 + (fraction > 0.875).int()).clamp(min=X8_MIN_EXP[dtype])
+    top = kept.abs().amax(2)
+    fraction, power = torch.frexp(top)
+    e = torch.where(top > 0.0, power - 9 + (fraction > 0.875).int(), X8_MIN_EXP[dtype]).clamp(min=X8_MIN_EXP[dtype])
     codes = torch.ldexp(kept, -e[..., None]).to(torch.float8_e4m3fn).float()
     return torch.where(fine, codes, torch.full_like(codes, float("nan"))), e
 
