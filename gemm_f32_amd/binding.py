@@ -111,6 +111,19 @@ def _load():
     lib.gemm_bf16_f32acc_noalloc.argtypes, lib.gemm_bf16_f32acc_noalloc.restype = args, ci
     lib.gemm_fp8_f32acc.argtypes = [i64, i64, i64, vp, i64, ci, ci, vp, i64, ci, ci, vp, i64, ci, vp]
     lib.gemm_fp8_f32acc.restype = ci
+    w4, x8, epi, size, cf = (ctypes.POINTER(W4Struct), ctypes.POINTER(X8Struct), ctypes.POINTER(EpilogueStruct),
+                             ctypes.c_size_t, ctypes.c_float)
+    for t in ("bf16", "f16"):
+        for name, a in ((f"gemm_{t}_w4_quantize", [i64, i64, vp, i64, w4, vp]),
+                        (f"gemm_{t}_w4_dequantize", [i64, i64, w4, vp, i64, vp]),
+                        (f"gemm_{t}_w4", [i64, i64, i64, vp, i64, w4, ci, vp, i64, epi, vp, size, vp]),
+                        (f"gemm_{t}_x8_quantize", [i64, i64, vp, i64, x8, vp]),
+                        (f"gemm_{t}_x8_dequantize", [i64, i64, x8, vp, i64, vp]),
+                        (f"gemm_{t}_x8_wgrad", [i64, i64, i64, vp, i64, x8, vp, i64, cf, cf, ci, vp, size, vp])):
+            f = getattr(lib, name)
+            f.argtypes, f.restype = a, ci
+    lib.gemm_w4_workspace_size.argtypes, lib.gemm_w4_workspace_size.restype = [i64, i64, i64, ci], size
+    lib.gemm_x8_wgrad_workspace_size.argtypes, lib.gemm_x8_wgrad_workspace_size.restype = [i64, i64, i64], size
     return lib
 
 
@@ -125,6 +138,7 @@ class Out(enum.IntEnum):
     """gemm_out_t"""
     F32 = 0
     BF16 = 1
+    F16 = 2              # the calls on low-bit operands only
 
 
 class EpilogueStruct(ctypes.Structure):
@@ -133,13 +147,31 @@ class EpilogueStruct(ctypes.Structure):
                 ("activation", ctypes.c_int), ("out_type", ctypes.c_int)]
 
 
+class W4Struct(ctypes.Structure):
+    """gemm_w4_t"""
+    _fields_ = [("codes", ctypes.c_void_p), ("ld_codes", ctypes.c_int64), ("scales", ctypes.c_void_p),
+                ("ld_scales", ctypes.c_int64), ("zeros", ctypes.c_void_p), ("ld_zeros", ctypes.c_int64),
+                ("group", ctypes.c_int)]
+
+
+class X8Struct(ctypes.Structure):
+    """gemm_x8_t"""
+    _fields_ = [("codes", ctypes.c_void_p), ("ld_codes", ctypes.c_int64), ("exponents", ctypes.c_void_p),
+                ("ld_exponents", ctypes.c_int64)]
+
+
 EXPORTED = ("gemm_f32", "gemm_bf16_f32acc", "gemm_f32_algo", "gemm_bf16_f32acc_algo",
             "gemm_status_string", "gemm_last_hip_error", "gemm_last_kernel", "gemm_version",
             "gemm_plan", "gemm_workspace_size", "gemm_f32_ws", "gemm_bf16_f32acc_ws",
             "gemm_f16_f32acc", "gemm_f16_f32acc_algo", "gemm_f16_f32acc_ws",
             "gemm_f32_strided_batched", "gemm_bf16_f32acc_strided_batched",
             "gemm_f16_f32acc_strided_batched", "gemm_bf16_f32acc_fused", "gemm_f16_f32acc_fused",
-            "gemm_bf16_f32acc_noalloc", "gemm_fp8_f32acc", "gemm_f32_fused")
+            "gemm_bf16_f32acc_noalloc", "gemm_fp8_f32acc", "gemm_f32_fused",
+            "gemm_bf16_w4_quantize", "gemm_f16_w4_quantize", "gemm_bf16_w4_dequantize",
+            "gemm_f16_w4_dequantize", "gemm_w4_workspace_size", "gemm_bf16_w4", "gemm_f16_w4",
+            "gemm_bf16_x8_quantize", "gemm_f16_x8_quantize", "gemm_bf16_x8_dequantize",
+            "gemm_f16_x8_dequantize", "gemm_x8_wgrad_workspace_size", "gemm_bf16_x8_wgrad",
+            "gemm_f16_x8_wgrad")
 
 # bytes of the static scratch behind gemm_bf16_f32acc_noalloc (GEMM_NOALLOC_SCRATCH_BYTES)
 NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -255,6 +287,83 @@ def gemm_fp8_f32acc(M, N, K, A, lda, order_a, format_a, B, ldb, order_b, format_
     A row-major, B column-major."""
     _check(lib_handle().gemm_fp8_f32acc(M, N, K, A, lda, order_a, int(format_a), B, ldb, order_b, int(format_b),
                                         C, ldc, order_c, stream), "gemm_fp8_f32acc")
+
+
+# --- low-bit operands: W a W4Struct, X a X8Struct (device pointers inside) -----------------
+def gemm_bf16_w4_quantize(rows, cols, W, ldw, Q, stream=0):
+    """Round a bf16 matrix to the 4-bit codes, scales and zero points of Q (a W4Struct)."""
+    _check(lib_handle().gemm_bf16_w4_quantize(rows, cols, W, ldw, Q, stream), "gemm_bf16_w4_quantize")
+
+
+def gemm_f16_w4_quantize(rows, cols, W, ldw, Q, stream=0):
+    """gemm_bf16_w4_quantize for IEEE fp16."""
+    _check(lib_handle().gemm_f16_w4_quantize(rows, cols, W, ldw, Q, stream), "gemm_f16_w4_quantize")
+
+
+def gemm_bf16_w4_dequantize(rows, cols, Q, W, ldw, stream=0):
+    """The bf16 matrix that Q stands for."""
+    _check(lib_handle().gemm_bf16_w4_dequantize(rows, cols, Q, W, ldw, stream), "gemm_bf16_w4_dequantize")
+
+
+def gemm_f16_w4_dequantize(rows, cols, Q, W, ldw, stream=0):
+    """The fp16 matrix that Q stands for."""
+    _check(lib_handle().gemm_f16_w4_dequantize(rows, cols, Q, W, ldw, stream), "gemm_f16_w4_dequantize")
+
+
+def gemm_w4_workspace_size(M, N, K, order_b) -> int:
+    """Workspace bytes of gemm_*_w4 for these extents (0: it uses none)."""
+    return lib_handle().gemm_w4_workspace_size(M, N, K, order_b)
+
+
+def gemm_bf16_w4(M, N, K, A, lda, W, order_b, C, ldc, epilogue=None, workspace=0, workspace_bytes=0, stream=0):
+    """C = epilogue(A.B), A bf16, B in 4 bits (epilogue an EpilogueStruct or None)."""
+    _check(lib_handle().gemm_bf16_w4(M, N, K, A, lda, W, order_b, C, ldc, epilogue, workspace, workspace_bytes,
+                                     stream), "gemm_bf16_w4")
+
+
+def gemm_f16_w4(M, N, K, A, lda, W, order_b, C, ldc, epilogue=None, workspace=0, workspace_bytes=0, stream=0):
+    """gemm_bf16_w4 for IEEE fp16."""
+    _check(lib_handle().gemm_f16_w4(M, N, K, A, lda, W, order_b, C, ldc, epilogue, workspace, workspace_bytes,
+                                    stream), "gemm_f16_w4")
+
+
+def gemm_bf16_x8_quantize(rows, cols, X, ldx, Q, stream=0):
+    """Round a bf16 matrix to the E4M3 codes and exponents of Q (a X8Struct)."""
+    _check(lib_handle().gemm_bf16_x8_quantize(rows, cols, X, ldx, Q, stream), "gemm_bf16_x8_quantize")
+
+
+def gemm_f16_x8_quantize(rows, cols, X, ldx, Q, stream=0):
+    """gemm_bf16_x8_quantize for IEEE fp16."""
+    _check(lib_handle().gemm_f16_x8_quantize(rows, cols, X, ldx, Q, stream), "gemm_f16_x8_quantize")
+
+
+def gemm_bf16_x8_dequantize(rows, cols, Q, X, ldx, stream=0):
+    """The bf16 matrix that Q stands for."""
+    _check(lib_handle().gemm_bf16_x8_dequantize(rows, cols, Q, X, ldx, stream), "gemm_bf16_x8_dequantize")
+
+
+def gemm_f16_x8_dequantize(rows, cols, Q, X, ldx, stream=0):
+    """The fp16 matrix that Q stands for."""
+    _check(lib_handle().gemm_f16_x8_dequantize(rows, cols, Q, X, ldx, stream), "gemm_f16_x8_dequantize")
+
+
+def gemm_x8_wgrad_workspace_size(tokens, N, K) -> int:
+    """Workspace bytes that gemm_*_x8_wgrad needs for these extents."""
+    return lib_handle().gemm_x8_wgrad_workspace_size(tokens, N, K)
+
+
+def gemm_bf16_x8_wgrad(tokens, N, K, dY, lddy, X, C, ldc, alpha=1.0, beta=0.0, out_type=Out.F32, workspace=0,
+                       workspace_bytes=0, stream=0):
+    """C = alpha * dY^T . X + beta * C, dY bf16, X in 8 bits."""
+    _check(lib_handle().gemm_bf16_x8_wgrad(tokens, N, K, dY, lddy, X, C, ldc, alpha, beta, int(out_type), workspace,
+                                           workspace_bytes, stream), "gemm_bf16_x8_wgrad")
+
+
+def gemm_f16_x8_wgrad(tokens, N, K, dY, lddy, X, C, ldc, alpha=1.0, beta=0.0, out_type=Out.F32, workspace=0,
+                      workspace_bytes=0, stream=0):
+    """gemm_bf16_x8_wgrad for IEEE fp16."""
+    _check(lib_handle().gemm_f16_x8_wgrad(tokens, N, K, dY, lddy, X, C, ldc, alpha, beta, int(out_type), workspace,
+                                          workspace_bytes, stream), "gemm_f16_x8_wgrad")
 
 
 # --- torch tensors -> (pointer, leading dimension, order) ------------------------------

@@ -9,6 +9,7 @@
 #include <mutex>
 
 #include "gemm.h"
+#include "api_internal.hpp"
 #include "common.hpp"
 #include "launch.hpp"
 
@@ -25,8 +26,6 @@ namespace {
 
 thread_local int t_last_hip_error = 0;
 thread_local const char* t_last_kernel = "none";
-
-enum class In { F32, BF16, F16, FP8 };
 
 int elem_of(In in) {
     return in == In::F32 ? kElemF32 : in == In::BF16 ? kElemBf16 : in == In::F16 ? kElemF16 : kElemFp8;
@@ -784,6 +783,57 @@ gemm_status_t run_batched(In in, int64_t batch, int64_t M, int64_t N, int64_t K,
     return GEMM_OK;
 }
 
+// C = epilogue(A.B) on the direct-copy kernels, p normalised (its C is `C`, an element type per e.out)
+// and within their layouts, K >= 1: a core on one direct-copy tile and the strips that complete it,
+// every part on the direct-copy kernels (the only ones that carry the epilogue), each strip on its own
+// cheapest tile: 2048 x 11008 is 8 x 32 tiles of 256 x 256 (one round) and a 2048 x 2816 strip of
+// 256 x 128 tiles (one round), against 2.7 rounds of 256 x 128 tiles.
+hipError_t fused_tiles(In in, const Problem& p, const Epilogue& e, void* C, const DeviceInfo& dev, hipStream_t stream,
+                       const char*& name) {
+    const bool f32 = in == In::F32, tn = p.oa == kCol;
+    const bool identity = e.alpha == 1.f && e.beta == 0.f && e.bias == nullptr && e.act == kActNone && e.out == kOutF32;
+    const TileOpt* opts = f32 ? kF32DmaOpts : kBf16DmaOpts;
+    const StripPricer dma_strips{opts, 2, opts, 0, dev.cus};
+    Plan best;
+    for (int i = 0; i < 2; ++i) {
+        const Plan pl = plan_core(p, opts[i], true, true, dev.cus, dma_strips);
+        if (pl.cost < best.cost) best = pl;
+    }
+    const int eb = e.out == kOutF32 ? 4 : 2;
+    auto part = [&](int r0, int m, int c0, int n, const TileOpt* force) {
+        EpiProblem ep{};
+        static_cast<Problem&>(ep) = sub_problem(p, r0, m, c0, n, f32 ? 4 : 2);
+        ep.C = reinterpret_cast<float*>(static_cast<char*>(C) + ((int64_t)r0 * p.ldc + c0) * eb);
+        ep.e = e;
+        if (e.bias != nullptr) ep.e.bias = e.bias + (e.bias_rows ? r0 : c0);
+        TileOpt o = force != nullptr ? *force : opts[0];
+        if (force == nullptr) {
+            double c = 1e300;
+            for (int i = 0; i < 2; ++i) {
+                const double pc = plan_whole(ep, opts[i], dev.cus).cost;
+                if (pc < c) { c = pc; o = opts[i]; }
+            }
+        }
+        Launch l = launch_for(ep, stream);
+        l.vec_c = (p.ldc % 4 == 0) && aligned(ep.C, e.out == kOutF32 ? 16 : 8);
+        l.group_m = pick_group_m((m + o.bm - 1) / o.bm, (n + o.bn - 1) / o.bn);
+        if (f32) return launch_f32_dma_epi(ep, l, o.bm, o.bn);
+        if (tn) return launch_bf16_dma_tn(ep, l, o.bm, o.bn, in == In::F16);
+        return identity ? launch_bf16_dma(ep, l, o.bm, o.bn, in == In::F16)
+                        : launch_bf16_dma_epi(ep, l, o.bm, o.bn, in == In::F16);
+    };
+    hipError_t err = part(0, best.mc, 0, best.nc, &best.opt);
+    if (err == hipSuccess && best.mc < p.M) err = part(best.mc, p.M - best.mc, 0, p.N, nullptr);
+    if (err == hipSuccess && best.nc < p.N) err = part(0, best.mc, best.nc, p.N - best.nc, nullptr);
+    static const char* names[2][2][2] = {{{"bf16_dma256x256_fused", "bf16_dma256x128_fused"},
+                                          {"f16_dma256x256_fused", "f16_dma256x128_fused"}},
+                                         {{"bf16_dma256x256", "bf16_dma256x128"},
+                                          {"f16_dma256x256", "f16_dma256x128"}}};
+    name = f32 ? (best.opt.bn == 256 ? "f32_dma256x256_fused" : "f32_dma128x128_fused")
+               : names[identity ? 1 : 0][in == In::F16 ? 1 : 0][best.opt.bn == 256 ? 0 : 1];
+    return err;
+}
+
 // GEMM with the fused epilogue: 16-bit inputs on the direct-copy kernel, the whole of C in one
 // launch (tiles overhang both edges), or the epilogue of an empty sum for K == 0.
 gemm_status_t run_fused(In in, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, gemm_order_t oa,
@@ -816,7 +866,7 @@ gemm_status_t run_fused(In in, int64_t M, int64_t N, int64_t K, const void* A, i
     if (!device_info(dev) || !dev.supported) return GEMM_ERR_UNSUPPORTED_DEVICE;
 
     // a column-major C's bias runs along its columns, the rows of the normalised C
-    const Epilogue e{epi->alpha, epi->beta, epi->bias, row ? 0 : 1, (int)epi->activation, out16 ? 1 : 0};
+    const Epilogue e{epi->alpha, epi->beta, epi->bias, row ? 0 : 1, (int)epi->activation, out16 ? kOutBf16 : kOutF32};
     // nothing to apply: the plain kernel on the same plan (FP32 inputs: the plain call)
     const bool identity = e.alpha == 1.f && e.beta == 0.f && e.bias == nullptr && e.act == kActNone && !out16;
     if (identity && f32 && K > 0)
@@ -832,48 +882,7 @@ gemm_status_t run_fused(In in, int64_t M, int64_t N, int64_t K, const void* A, i
         l.vec_c = (p.ldc % 4 == 0) && aligned(C, out16 ? 8 : 16);
         err = launch_epi_fill(ep, l);
     } else {
-        // a core on one direct-copy tile and the strips that complete it, every part on the
-        // direct-copy kernels (the only ones that carry the epilogue), each strip on its own
-        // cheapest tile: 2048 x 11008 is 8 x 32 tiles of 256 x 256 (one round) and a 2048 x 2816
-        // strip of 256 x 128 tiles (one round), against 2.7 rounds of 256 x 128 tiles
-        const TileOpt* opts = f32 ? kF32DmaOpts : kBf16DmaOpts;
-        const StripPricer dma_strips{opts, 2, opts, 0, dev.cus};
-        Plan best;
-        for (int i = 0; i < 2; ++i) {
-            const Plan pl = plan_core(p, opts[i], true, true, dev.cus, dma_strips);
-            if (pl.cost < best.cost) best = pl;
-        }
-        const int eb = out16 ? 2 : 4;
-        auto part = [&](int r0, int m, int c0, int n, const TileOpt* force) {
-            EpiProblem ep{};
-            static_cast<Problem&>(ep) = sub_problem(p, r0, m, c0, n, f32 ? 4 : 2);
-            ep.C = reinterpret_cast<float*>(static_cast<char*>(C) + ((int64_t)r0 * p.ldc + c0) * eb);
-            ep.e = e;
-            if (e.bias != nullptr) ep.e.bias = e.bias + (e.bias_rows ? r0 : c0);
-            TileOpt o = force != nullptr ? *force : opts[0];
-            if (force == nullptr) {
-                double c = 1e300;
-                for (int i = 0; i < 2; ++i) {
-                    const double pc = plan_whole(ep, opts[i], dev.cus).cost;
-                    if (pc < c) { c = pc; o = opts[i]; }
-                }
-            }
-            Launch l = launch_for(ep, stream);
-            l.vec_c = (p.ldc % 4 == 0) && aligned(ep.C, out16 ? 8 : 16);
-            l.group_m = pick_group_m((m + o.bm - 1) / o.bm, (n + o.bn - 1) / o.bn);
-            if (f32) return launch_f32_dma_epi(ep, l, o.bm, o.bn);
-            return identity ? launch_bf16_dma(ep, l, o.bm, o.bn, in == In::F16)
-                            : launch_bf16_dma_epi(ep, l, o.bm, o.bn, in == In::F16);
-        };
-        err = part(0, best.mc, 0, best.nc, &best.opt);
-        if (err == hipSuccess && best.mc < p.M) err = part(best.mc, p.M - best.mc, 0, p.N, nullptr);
-        if (err == hipSuccess && best.nc < p.N) err = part(0, best.mc, best.nc, p.N - best.nc, nullptr);
-        static const char* names[2][2][2] = {{{"bf16_dma256x256_fused", "bf16_dma256x128_fused"},
-                                              {"f16_dma256x256_fused", "f16_dma256x128_fused"}},
-                                             {{"bf16_dma256x256", "bf16_dma256x128"},
-                                              {"f16_dma256x256", "f16_dma256x128"}}};
-        name = f32 ? (best.opt.bn == 256 ? "f32_dma256x256_fused" : "f32_dma128x128_fused")
-                   : names[identity ? 1 : 0][in == In::F16 ? 1 : 0][best.opt.bn == 256 ? 0 : 1];
+        err = fused_tiles(in, p, e, C, dev, stream, name);
     }
     if (err != hipSuccess) {
         t_last_hip_error = (int)err;
@@ -954,6 +963,39 @@ gemm_status_t run_noalloc(int64_t M, int64_t N, int64_t K, const uint16_t* A, in
 }
 
 }  // namespace
+
+bool current_device(int& cus) {
+    DeviceInfo dev;
+    if (!device_info(dev) || !dev.supported) return false;
+    cus = dev.cus;
+    return true;
+}
+
+gemm_status_t record_call(hipError_t err, const char* name) {
+    if (err != hipSuccess) {
+        t_last_hip_error = (int)err;
+        return GEMM_ERR_LAUNCH;
+    }
+    t_last_kernel = name;
+    return GEMM_OK;
+}
+
+hipError_t run_fused_tiles(In in, const Problem& p, const Epilogue& e, void* C, int cus, hipStream_t stream,
+                           const char*& name) {
+    DeviceInfo dev;
+    dev.supported = true;
+    dev.cus = cus;
+    return fused_tiles(in, p, e, C, dev, stream, name);
+}
+
+hipError_t run_epilogue_fill(const Problem& p, const Epilogue& e, void* C, hipStream_t stream) {
+    EpiProblem ep{};
+    static_cast<Problem&>(ep) = p;
+    ep.C = static_cast<float*>(C);
+    ep.e = e;
+    return launch_epi_fill(ep, launch_for(ep, stream));
+}
+
 }  // namespace gemm
 
 extern "C" {

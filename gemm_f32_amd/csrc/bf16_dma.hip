@@ -148,13 +148,18 @@ using Cfg256x128F8 = Cfg<256, 128, 4, 2, 2, 3, false, 1>;
 // memory, BK k-rows of BN columns, and read with gfx950's transposing LDS read, which hands each
 // lane four consecutive k of one column (the layout of the B tile and its reads are described at
 // the copy plan below).
-template <typename C, bool VEC_C, int IT, int MODE, bool TK = false, bool BRM = false>
+// ARM: column-major A (m contiguous) held and read the same way, beside a row-major B: the product
+// over tokens of a weight gradient, dY^T . X, both operands as they lie in memory.  Columns of both
+// are then read in whole chunks of 8, the last of them past M or N (the host makes sure that they
+// can be read; what they hold reaches no stored output).
+template <typename C, bool VEC_C, int IT, int MODE, bool TK = false, bool BRM = false, bool ARM = false>
 __global__ __launch_bounds__(C::THREADS) __attribute__((amdgpu_waves_per_eu(C::NW / 4, C::NW / 4)))
 void k_bf16_dma(typename ModeArgT<MODE>::type p, int tiles_m, int tiles_n, int group_m) {
     constexpr bool BATCH = MODE == kBatched, EPI = MODE == kEpilogue;
     static_assert((IT >= kInFp8) == (C::ES == 1), "8-bit inputs take the 8-bit configurations");
     static_assert(!TK || C::ES == 1, "byte-wise K tail for 8-bit inputs only");
     static_assert(!BRM || C::ES == 2, "row-major B for 16-bit inputs only");
+    static_assert(!ARM || BRM, "column-major A beside a row-major B only");
     constexpr int ES = C::ES;
     constexpr int BM = C::BM, BN = C::BN, BK = C::BK, FM = C::FM, FN = C::FN, SUB = C::SUB;
     constexpr int ROW = C::ROW, MF = C::MF;
@@ -197,7 +202,7 @@ void k_bf16_dma(typename ModeArgT<MODE>::type p, int tiles_m, int tiles_n, int g
     const int arow0 = m0 + wave * C::A_RPW, brow0 = n0 + wave * C::B_RPW;
     // (wavefront-uniform values; readfirstlane tells the compiler so, which keeps the buffer
     // resources in scalar registers)
-    const int avalid = __builtin_amdgcn_readfirstlane(max(0, min(C::A_RPW, p.M - arow0)));
+    const int avalid = ARM ? 0 : __builtin_amdgcn_readfirstlane(max(0, min(C::A_RPW, p.M - arow0)));
     const int bvalid = __builtin_amdgcn_readfirstlane(max(0, min(C::B_RPW, p.N - brow0)));
     const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
         (void*)(avalid > 0 ? A + (int64_t)arow0 * p.lda * ES : A), (short)0, (int)(avalid * p.lda * ES), kBufWord3);
@@ -222,10 +227,13 @@ void k_bf16_dma(typename ModeArgT<MODE>::type p, int tiles_m, int tiles_n, int g
     auto bsw = [](int kr) { return ((kr & 3) | ((kr >> 1) & 4)) & GM; };
     const int lr2 = lane / (RP / 16), cc2 = lane % (RP / 16);
     const int bsw_w = __builtin_amdgcn_readfirstlane(bsw(wave * KRW));
+    // columns of B that can be read (a row-major B from the caller has N % 8 == 0; the 16-bit numbers of a
+    // low-bit operand lie in rows of a multiple of 8)
+    const int n_read = (p.N + 7) & ~7;
     // offset of this lane's 16 bytes from the wavefront's first k-row of the k-tile, for a copy
     // whose k-rows have pattern f
     auto brm_lane = [&](int f) -> unsigned {
-        const int col = min(n0 + 8 * (cc2 ^ (4 * (bsw(lr2) ^ f))), p.N - 8);
+        const int col = min(n0 + 8 * (cc2 ^ (4 * (bsw(lr2) ^ f))), n_read - 8);
         return (unsigned)(lr2 * (int)p.ldb * 2 + 2 * (col - n0));
     };
     // the resource starts at the wavefront's first k-row, column n0, and ends after element
@@ -233,7 +241,7 @@ void k_bf16_dma(typename ModeArgT<MODE>::type p, int tiles_m, int tiles_n, int g
     const int brm_row0 = wave * KRW;
     const __amdgpu_buffer_rsrc_t rbr = __builtin_amdgcn_make_buffer_rsrc(
         (void*)(B + ((int64_t)brm_row0 * p.ldb + n0) * 2), (short)0,
-        (int)(((int64_t)(p.K - 1 - brm_row0) * p.ldb + p.N - n0) * 2), kBufWord3);
+        (int)(((int64_t)(p.K - 1 - brm_row0) * p.ldb + n_read - n0) * 2), kBufWord3);
     const int brm_kt = BK * (int)p.ldb * 2, brm_step = RPC2 * (int)p.ldb * 2;   // per k-tile, per copy
     // B copy jb of k-tile kt into the LDS block at dst
     // (offsets as named values: with the lambda call inside the builtin's argument list the host
@@ -246,6 +254,30 @@ void k_bf16_dma(typename ModeArgT<MODE>::type p, int tiles_m, int tiles_n, int g
         } else
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, dst, 16, boff[jb & 1] + jb * bstep, kt * ROW, 0, 0);
     };
+    // ---- column-major A (ARM): the same layout, copies and reads for the BK k-rows of BM rows of C
+    // that the A tile holds (RPA bytes each)
+    constexpr int RPA = BM * 2, RPCA = 1024 / RPA, GMA = RPA / 64 - 1;
+    auto asw = [&](int kr) { return ((kr & 3) | ((kr >> 1) & 4)) & GMA; };
+    const int m_read = (p.M + 7) & ~7;                  // rows of A that can be read
+    const int lra = lane / (RPA / 16), cca = lane % (RPA / 16);
+    const int asw_w = __builtin_amdgcn_readfirstlane(asw(wave * KRW));
+    auto arm_lane = [&](int f) -> unsigned {
+        const int row = min(m0 + 8 * (cca ^ (4 * (asw(lra) ^ f))), m_read - 8);
+        return (unsigned)(lra * (int)p.lda * 2 + 2 * (row - m0));
+    };
+    const __amdgpu_buffer_rsrc_t rar = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(A + (ARM ? ((int64_t)brm_row0 * p.lda + m0) * 2 : 0)), (short)0,
+        (int)(ARM ? ((int64_t)(p.K - 1 - brm_row0) * p.lda + m_read - m0) * 2 : 0), kBufWord3);
+    const int arm_kt = BK * (int)p.lda * 2, arm_step = RPCA * (int)p.lda * 2;
+    // A copy j of k-tile kt into the LDS block at dst
+    auto copy_a = [&](int j, int kt, lds_void* dst) {
+        if constexpr (ARM) {
+            const unsigned vo = arm_lane(asw_w ^ asw(j * RPCA));
+            const int so = kt * arm_kt + j * arm_step;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rar, dst, 16, vo, so, 0, 0);
+        } else
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, dst, 16, aoff[j & 1] + j * astep, kt * ROW, 0, 0);
+    };
     // copy j (of DMA) of k-tile kt (source) into stage st.  (The LDS pointer is a named
     // variable: cast inline in the builtin's argument list, the host pass of this compiler
     // silently drops the kernel's launch stub.)
@@ -256,7 +288,7 @@ void k_bf16_dma(typename ModeArgT<MODE>::type p, int tiles_m, int tiles_n, int g
         unsigned char* s = smem + st * C::STAGE;
         if (j < C::A_DMA) {
             lds_void* dst = (lds_void*)(s + (wave * C::A_DMA + j) * 1024);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, dst, 16, aoff[j & 1] + j * astep, kt * ROW, 0, 0);
+            copy_a(j, kt, dst);
         } else {
             const int jb = j - C::A_DMA;
             lds_void* dst = (lds_void*)(s + C::A_BYTES + (wave * C::B_DMA + jb) * 1024);
@@ -317,6 +349,18 @@ void k_bf16_dma(typename ModeArgT<MODE>::type p, int tiles_m, int tiles_n, int g
         const s16x4 hi = lds_read_tr16((lds_s16x4*)(q + 4 * RP));
         return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     };
+    // A fragment i at k-step s of the A tile at LDS offset `tile`
+    const unsigned arm_rd = (unsigned)(brm_kr * RPA + (((wm >> 5) ^ asw(brm_kr)) << 6) + 32 * ((lane >> 4) & 1) +
+                                       8 * (l16 & 3));
+    auto frag_a = [&](int tile, int s, int i) -> Frag {
+        if constexpr (ARM) {
+            const unsigned char* q = smem + ((unsigned)(tile + arm_rd) ^ (unsigned)(i << 6)) + 16 * s * RPA;
+            const s16x4 lo = lds_read_tr16((lds_s16x4*)q);
+            const s16x4 hi = lds_read_tr16((lds_s16x4*)(q + 4 * RPA));
+            return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        } else
+            return frag_at(smem + tile + a_off + i * 32 * ROW, s);
+    };
     // B fragment j at k-step s of the B tile at LDS offset `tile`
     auto frag_b = [&](int tile, int s, int j) -> Frag {
         if constexpr (BRM) return frag_rm(tile, s, j);
@@ -324,8 +368,7 @@ void k_bf16_dma(typename ModeArgT<MODE>::type p, int tiles_m, int tiles_n, int g
     };
     // fragment read `m` (A fragments first, then B) of k-step s of stage st into buffer b
     auto read_slot = [&](int st, int s, int m, int b) {
-        const unsigned char* base = smem + st * C::STAGE;
-        if (m < FM) fa[b][m] = frag_at(base + a_off + m * 32 * ROW, s);
+        if (m < FM) fa[b][m] = frag_a(st * C::STAGE, s, m);
         else if (m < C::RD) fb[b][m - FM] = frag_b(st * C::STAGE + C::A_BYTES, s, m - FM);
     };
     auto mfma = [&](int m, int b) {
@@ -366,12 +409,12 @@ void k_bf16_dma(typename ModeArgT<MODE>::type p, int tiles_m, int tiles_n, int g
         if (nk > 0) {                         // uniform
             const int last = nk - 1;
             auto read_ring = [&](int abuf, int bbuf, int s, int m, int b) {
-                if (m < FM) fa[b][m] = frag_at(smem + abuf * C::A_BYTES + a_off + m * 32 * ROW, s);
+                if (m < FM) fa[b][m] = frag_a(abuf * C::A_BYTES, s, m);
                 else if (m < C::RD) fb[b][m - FM] = frag_b(bbuf * C::A_BYTES, s, m - FM);
             };
             auto issue_a = [&](int j, int kt, int buf) {
                 lds_void* dst = (lds_void*)(smem + buf * C::A_BYTES + (wave * C::A_DMA + j) * 1024);
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, dst, 16, aoff[j & 1] + j * astep, kt * ROW, 0, 0);
+                copy_a(j, kt, dst);
             };
             auto issue_b = [&](int j, int kt, int buf) {
                 lds_void* dst = (lds_void*)(smem + buf * C::A_BYTES + (wave * C::B_DMA + j) * 1024);
@@ -504,8 +547,16 @@ void k_bf16_dma(typename ModeArgT<MODE>::type p, int tiles_m, int tiles_n, int g
             const int lt = lane_id();         // (formed anew, as in the epilogue)
             const int kr = brm_row0 + jb * RPC2 + lt / (RP / 16);
             const int n = n0 + 8 * ((lt % (RP / 16)) ^ (4 * bsw(kr)));
-            src = B + ((int64_t)min(k0 + kr, p.K - 1) * p.ldb + min(n, p.N - 8)) * 2;
+            src = B + ((int64_t)min(k0 + kr, p.K - 1) * p.ldb + min(n, n_read - 8)) * 2;
             keep = k0 + kr < p.K && n < p.N;
+        };
+        // ARM: A chunk j of the copy plan
+        auto chunk_am = [&](int j, const unsigned char*& src, bool& keep) {
+            const int lt = lane_id();
+            const int kr = brm_row0 + j * RPCA + lt / (RPA / 16);
+            const int m = m0 + 8 * ((lt % (RPA / 16)) ^ (4 * asw(kr)));
+            src = A + ((int64_t)min(k0 + kr, p.K - 1) * p.lda + min(m, m_read - 8)) * 2;
+            keep = k0 + kr < p.K && m < p.M;
         };
         if constexpr (!TK) {                  // K >= CE (16-bit inputs: K >= 64)
 #pragma unroll
@@ -513,6 +564,11 @@ void k_bf16_dma(typename ModeArgT<MODE>::type p, int tiles_m, int tiles_n, int g
                 const unsigned char* src; int k; bool keep;
                 if (BRM && j >= C::A_DMA) {
                     chunk_rm(j - C::A_DMA, src, keep);
+                    v[j] = load16(src);
+                    continue;
+                }
+                if (ARM) {
+                    chunk_am(j, src, keep);
                     v[j] = load16(src);
                     continue;
                 }
@@ -524,6 +580,11 @@ void k_bf16_dma(typename ModeArgT<MODE>::type p, int tiles_m, int tiles_n, int g
                 const unsigned char* src; int k; bool keep;
                 if (BRM && j >= C::A_DMA) {       // whole k-rows: keep or clear
                     chunk_rm(j - C::A_DMA, src, keep);
+                    if (!keep) v[j] = make_uint4(0u, 0u, 0u, 0u);
+                    continue;
+                }
+                if (ARM) {
+                    chunk_am(j, src, keep);
                     if (!keep) v[j] = make_uint4(0u, 0u, 0u, 0u);
                     continue;
                 }
@@ -795,6 +856,36 @@ hipError_t launch_bf16_dma(const Problem& p, const Launch& l, int bm, int bn, bo
 hipError_t launch_bf16_dma_epi(const EpiProblem& p, const Launch& l, int bm, int bn, bool f16) {
     if (bm == 256 && bn == 256) return launch_cfg<Cfg256, kEpilogue>(p, l, in16(f16));
     if (bm == 256 && bn == 128) return launch_cfg<Cfg<256, 128, 4, 2, 4, 3>, kEpilogue>(p, l, in16(f16));
+    return hipErrorInvalidValue;
+}
+
+// The weight gradient's layout: column-major A and row-major B (ARM), any M and N whose rows of A and
+// columns of B can be read up to the next multiple of 8, any K >= 1 (fewer than 64: the K tail alone).
+template <typename C>
+static hipError_t launch_tn(const EpiProblem& p, const Launch& l, bool f16) {
+    const int tiles_m = (p.M + C::BM - 1) / C::BM, tiles_n = (p.N + C::BN - 1) / C::BN;
+    auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3((unsigned)tiles_m * tiles_n), dim3(C::THREADS), 0, l.stream, p, tiles_m,
+                           tiles_n, l.group_m);
+        return hipGetLastError();
+    };
+    if (f16)
+        return l.vec_c ? go(k_bf16_dma<C, true, kInF16, kEpilogue, false, true, true>)
+                       : go(k_bf16_dma<C, false, kInF16, kEpilogue, false, true, true>);
+    return l.vec_c ? go(k_bf16_dma<C, true, kInBf16, kEpilogue, false, true, true>)
+                   : go(k_bf16_dma<C, false, kInBf16, kEpilogue, false, true, true>);
+}
+
+bool bf16_dma_tn_applies(const Problem& p) {
+    // byte offsets of both operands up to their last element below 2^31
+    const int64_t lim = (int64_t)1 << 31;
+    return p.oa == kCol && p.ob == kRow && p.K >= 1 && ((int64_t)(p.K - 1) * p.lda + p.M + 7) * 2 < lim &&
+           ((int64_t)(p.K - 1) * p.ldb + p.N + 7) * 2 < lim;
+}
+
+hipError_t launch_bf16_dma_tn(const EpiProblem& p, const Launch& l, int bm, int bn, bool f16) {
+    if (bm == 256 && bn == 256) return launch_tn<Cfg256>(p, l, f16);
+    if (bm == 256 && bn == 128) return launch_tn<Cfg<256, 128, 4, 2, 4, 3>>(p, l, f16);
     return hipErrorInvalidValue;
 }
 

@@ -1,5 +1,5 @@
 // Fused epilogue: C = act(alpha * acc + beta * C + bias), applied to each value on its way from the
-// accumulators to C (after the kernel's staging through LDS), with C stored as FP32 or as bf16 ("How a Matrix Multiply Runs on a GPU",
+// accumulators to C (after the kernel's staging through LDS), with C stored as FP32, bf16 or fp16 ("How a Matrix Multiply Runs on a GPU",
 // section "Level 2", the epilogue line of its block-tile loop, and section "Operational guidance
 // and trade-offs": bias, activation and casts belong in the epilogue; "A06 - Tiled Matrix
 // Multiply (GEMM)", section "6. Challenges, Drawbacks & Tradeoffs": fusion is what a hand-written
@@ -11,13 +11,14 @@
 namespace gemm {
 
 constexpr int kActNone = 0, kActRelu = 1, kActGelu = 2;
+constexpr int kOutF32 = 0, kOutBf16 = 1, kOutF16 = 2;
 
 struct Epilogue {
     float alpha, beta;
     const float* bias;   // nullptr: no bias
     int bias_rows;       // bias indexed by row of the normalised C (a column-major C's columns)
     int act;             // kActNone, kActRelu, kActGelu
-    int out_bf16;        // C holds bf16 bit patterns (2 bytes per element, ldc in elements)
+    int out;             // element of C: kOutF32, kOutBf16 or kOutF16 (bit patterns, ldc in elements)
 };
 
 // The kernel argument of an epilogue launch: the problem (C as raw memory) plus the epilogue.
@@ -28,8 +29,9 @@ template <> struct ModeArgT<kEpilogue> { using type = EpiProblem; };
 
 // C's previous value at element offset off, as FP32.
 __device__ __forceinline__ float epi_load(const Epilogue& e, const void* C, int64_t off) {
-    return e.out_bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(C)[off] << 16)
-                      : static_cast<const float*>(C)[off];
+    if (e.out == kOutF32) return static_cast<const float*>(C)[off];
+    const uint16_t u = static_cast<const uint16_t*>(C)[off];
+    return e.out == kOutBf16 ? __uint_as_float((uint32_t)u << 16) : (float)__builtin_bit_cast(_Float16, u);
 }
 
 // x * Phi(x), Phi the standard normal distribution function written through erf:
@@ -62,14 +64,14 @@ __device__ __forceinline__ float epi_value(const Epilogue& e, float acc, const v
     return y;
 }
 
-// Four consecutive previous values of a row of C (off 16-byte aligned for FP32 C, 8-byte for bf16 C).
+// Four consecutive previous values of a row of C (off 16-byte aligned for FP32 C, 8-byte for 16-bit C).
 __device__ __forceinline__ void epi_load4(const Epilogue& e, const void* C, int64_t off, float (&old)[4]) {
-    if (e.out_bf16) {
+    if (e.out != kOutF32) {
         const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(C) + off);
-        old[0] = __uint_as_float(u.x << 16);
-        old[1] = __uint_as_float(u.x & 0xffff0000u);
-        old[2] = __uint_as_float(u.y << 16);
-        old[3] = __uint_as_float(u.y & 0xffff0000u);
+        const uint32_t h[4] = {u.x & 0xffffu, u.x >> 16, u.y & 0xffffu, u.y >> 16};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            old[i] = e.out == kOutBf16 ? __uint_as_float(h[i] << 16) : (float)__builtin_bit_cast(_Float16, (uint16_t)h[i]);
     } else {
         const float4 f = *reinterpret_cast<const float4*>(static_cast<const float*>(C) + off);
         old[0] = f.x;
@@ -96,17 +98,27 @@ __device__ __forceinline__ uint16_t to_bf16(float y) {
     return __builtin_bit_cast(uint16_t, static_cast<__bf16>(y));
 }
 
+// The same for fp16 (the conversion instruction rounds to nearest, ties to even).
+__device__ __forceinline__ uint16_t to_f16(float y) {
+    return __builtin_bit_cast(uint16_t, static_cast<_Float16>(y));
+}
+
+// FP32 -> the bit pattern of a 16-bit C.
+__device__ __forceinline__ uint16_t to_16(const Epilogue& e, float y) {
+    return e.out == kOutBf16 ? to_bf16(y) : to_f16(y);
+}
+
 // Store one output value at element offset off of C.
 __device__ __forceinline__ void epi_store(const Epilogue& e, void* C, int64_t off, float y) {
-    if (e.out_bf16) static_cast<uint16_t*>(C)[off] = to_bf16(y);
+    if (e.out != kOutF32) static_cast<uint16_t*>(C)[off] = to_16(e, y);
     else static_cast<float*>(C)[off] = y;
 }
 
-// Four consecutive values of a row (16-byte aligned FP32 / 8-byte aligned bf16 C).
+// Four consecutive values of a row (16-byte aligned FP32 / 8-byte aligned 16-bit C).
 __device__ __forceinline__ void epi_store4(const Epilogue& e, void* C, int64_t off, const float (&y)[4]) {
-    if (e.out_bf16) {
-        const uint32_t lo = to_bf16(y[0]) | ((uint32_t)to_bf16(y[1]) << 16);
-        const uint32_t hi = to_bf16(y[2]) | ((uint32_t)to_bf16(y[3]) << 16);
+    if (e.out != kOutF32) {
+        const uint32_t lo = to_16(e, y[0]) | ((uint32_t)to_16(e, y[1]) << 16);
+        const uint32_t hi = to_16(e, y[2]) | ((uint32_t)to_16(e, y[3]) << 16);
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(C) + off) = make_uint2(lo, hi);
     } else {
         *reinterpret_cast<float4*>(static_cast<float*>(C) + off) = make_float4(y[0], y[1], y[2], y[3]);

@@ -88,6 +88,10 @@ hipError_t launch_zero_c(const Problem& p, const Launch& l);
 // and the epilogue of an empty sum for K == 0 (fill.hip)
 hipError_t launch_bf16_dma_epi(const EpiProblem& p, const Launch& l, int bm, int bn, bool f16);
 hipError_t launch_epi_fill(const EpiProblem& p, const Launch& l);
+// The 16-bit direct-copy kernel on a column-major A and a row-major B (a weight gradient's layout), with
+// the epilogue: any K >= 1; rows of A and columns of B must be readable up to the next multiple of 8.
+bool bf16_dma_tn_applies(const Problem& p);
+hipError_t launch_bf16_dma_tn(const EpiProblem& p, const Launch& l, int bm, int bn, bool f16);
 // Split-K on the 16-bit direct-copy kernel (same requirements as launch_bf16_dma, every slice
 // K >= 64): `slices` K slices of s.kslice as a second grid dimension, slices 1 .. S-1 into the
 // slabs at s.part, then launch_add_slabs (fill.hip) adds them to C in slice order.

@@ -1,0 +1,121 @@
+// Low-bit operands: 4-bit weights with a scale (and a zero point) per group of columns, and 8-bit
+// activations with an exponent per 32 columns.  Their formats, the conversions between codes and
+// the 16-bit numbers they stand for, and the launchers of lowbit_codec.hip and w4_rows.hip.
+//
+// Both decode to a 16-bit number T (bf16 or fp16), and every product reads exactly these numbers: a
+// 4-bit code c of a group with scale s and zero point z stands for the T nearest to (c - z) s (the
+// product of an integer of at most 8 bits and an 8- or 11-bit fraction is exact in FP32, so this is
+// one rounding, of half a step); an 8-bit code stands for e4m3(code) 2^e, which is a T.
+#pragma once
+
+#include "common.hpp"
+#include "epilogue.hpp"
+
+namespace gemm {
+
+// A 4-bit matrix of rows x cols as kernels see it.  codes: two to a byte along a row, even columns
+// in the low half; scales: T bit patterns; zeros: one byte per group, nullptr: 8 everywhere.  The
+// group of column c is c >> gshift.
+struct W4View {
+    const uint8_t* codes;
+    int64_t ld;
+    const uint16_t* scales;
+    int64_t lds;
+    const uint8_t* zeros;
+    int64_t ldz;
+    int gshift;
+};
+
+// 8-bit activations: E4M3 codes and one exponent byte (e + 127) per group of 32 columns.
+struct X8View {
+    const uint8_t* codes;
+    int64_t ld;
+    const uint8_t* exps;
+    int64_t lde;
+};
+
+// C (M x N, row-major) = epilogue(A . B), A 16-bit row-major, B 4-bit: stored N x K, groups along k
+// (tr == 0: a layer's forward product x . W^T) or K x N, groups along n (tr == 1: dy . W).
+struct W4Problem {
+    int M, N, K;
+    const uint16_t* A;
+    int64_t lda;
+    W4View w;
+    int tr;
+    void* C;
+    int64_t ldc;
+    Epilogue e;
+};
+
+hipError_t launch_w4_quantize(const uint16_t* W, int64_t ldw, int rows, int cols, const W4View& q, bool f16,
+                              hipStream_t stream);
+// out: T, leading dimension ldo
+hipError_t launch_w4_dequantize(const W4View& q, int rows, int cols, uint16_t* out, int64_t ldo, bool f16,
+                                hipStream_t stream);
+hipError_t launch_x8_quantize(const uint16_t* X, int64_t ldx, int rows, int cols, const X8View& q, bool f16,
+                              hipStream_t stream);
+hipError_t launch_x8_dequantize(const X8View& q, int rows, int cols, uint16_t* out, int64_t ldo, bool f16,
+                                hipStream_t stream);
+// rows x cols 16-bit elements into rows of ldo elements
+hipError_t launch_copy16(const uint16_t* in, int64_t ldi, int rows, int cols, uint16_t* out, int64_t ldo,
+                         hipStream_t stream);
+// The few-row kernel (w4_rows.hip): any M, N, K >= 1.
+hipError_t launch_w4_rows(const W4Problem& p, bool f16, int cus, hipStream_t stream, const char*& name);
+
+#ifdef __HIPCC__
+typedef float lb_f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 lb_bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 lb_f16x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32_ua __attribute__((aligned(1)));
+typedef uint16_t u16_ua __attribute__((aligned(1)));
+typedef unsigned int u32x2_ua __attribute__((ext_vector_type(2), aligned(1)));
+typedef unsigned int u32x4_ub __attribute__((ext_vector_type(4), aligned(1)));
+
+// two FP32 values -> two T, each to nearest, ties to even (one conversion instruction)
+template <bool F16>
+__device__ __forceinline__ uint32_t pack16(float a, float b) {
+    const lb_f32x2 v = {a, b};
+    if constexpr (F16) return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, lb_f16x2));
+    else return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, lb_bf16x2));
+}
+
+template <bool F16>
+__device__ __forceinline__ float from16(uint16_t u) {
+    if constexpr (F16) return (float)__builtin_bit_cast(_Float16, u);
+    else return __uint_as_float((uint32_t)u << 16);
+}
+
+template <bool F16>
+__device__ __forceinline__ uint16_t to16(float y) {
+    if constexpr (F16) return to_f16(y);
+    else return to_bf16(y);
+}
+
+// byte i of w as a float
+template <int I>
+__device__ __forceinline__ float ubyte(uint32_t w) {
+    return (float)((w >> (8 * I)) & 0xffu);
+}
+
+// Eight codes of one group (nibble i of w: column i) as T, in column order.  c s - z s is formed in
+// FP32: both products and their difference are exact, so the conversion's rounding is the only one.
+template <bool F16>
+__device__ __forceinline__ uint4 w4_eight(uint32_t w, float s, float minus_zs) {
+    const uint32_t lo = w & 0x0f0f0f0fu, hi = (w >> 4) & 0x0f0f0f0fu;
+    uint4 r;
+    r.x = pack16<F16>(fmaf(ubyte<0>(lo), s, minus_zs), fmaf(ubyte<0>(hi), s, minus_zs));
+    r.y = pack16<F16>(fmaf(ubyte<1>(lo), s, minus_zs), fmaf(ubyte<1>(hi), s, minus_zs));
+    r.z = pack16<F16>(fmaf(ubyte<2>(lo), s, minus_zs), fmaf(ubyte<2>(hi), s, minus_zs));
+    r.w = pack16<F16>(fmaf(ubyte<3>(lo), s, minus_zs), fmaf(ubyte<3>(hi), s, minus_zs));
+    return r;
+}
+
+// Four E4M3 codes times 2^e, f = 2^e, as T (exact for codes and exponents that launch_x8_quantize writes)
+template <bool F16>
+__device__ __forceinline__ uint2 x8_four(uint32_t w, float f) {
+    const lb_f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false), b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
+    return make_uint2(pack16<F16>(a.x * f, a.y * f), pack16<F16>(b.x * f, b.y * f));
+}
+#endif
+
+}  // namespace gemm

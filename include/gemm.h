@@ -349,9 +349,10 @@ gemm_status_t gemm_f16_f32acc_strided_batched(int64_t batch, int64_t M, int64_t 
  *   activation    GEMM_ACT_NONE; GEMM_ACT_RELU max(x, 0); GEMM_ACT_GELU x * Phi(x), Phi the
  *                 standard normal distribution function (the erf form), applied last
  *   out_type      GEMM_OUT_F32: C is float; GEMM_OUT_BF16: C holds bf16 bit patterns
- *                 (uint16_t), rounded to nearest even from the FP32 result, ldc in elements */
+ *                 (uint16_t), rounded to nearest even from the FP32 result, ldc in elements;
+ *                 GEMM_OUT_F16: the same in fp16 (the calls on low-bit operands below only) */
 typedef enum { GEMM_ACT_NONE = 0, GEMM_ACT_RELU = 1, GEMM_ACT_GELU = 2 } gemm_activation_t;
-typedef enum { GEMM_OUT_F32 = 0, GEMM_OUT_BF16 = 1 } gemm_out_t;
+typedef enum { GEMM_OUT_F32 = 0, GEMM_OUT_BF16 = 1, GEMM_OUT_F16 = 2 } gemm_out_t;
 typedef struct {
     float alpha;
     float beta;
@@ -411,6 +412,129 @@ gemm_status_t gemm_bf16_f32acc_noalloc(int64_t M, int64_t N, int64_t K,
                                        const uint16_t *B, int64_t ldb, gemm_order_t order_b,
                                        float *C, int64_t ldc, gemm_order_t order_c,
                                        hipStream_t stream);
+
+/* ---- Low-bit operands: 4-bit weights with group scales ------------------------------------
+ * Quantized inference runs the same GEMM on a narrower operand type ("A06 - Tiled Matrix Multiply
+ * (GEMM)", section 7, "Real-World Use Cases"); with few rows the product is bound by reading the
+ * weights ("How a Matrix Multiply Runs on a GPU", "Shapes that run slowly, and why"), which 4-bit
+ * codes make a quarter as long.  T is the 16-bit type in the call's name: bf16 or fp16.
+ *
+ * A gemm_w4_t is a rows x cols matrix (of a layer x . W^T: output features x input features) in 4-bit
+ * codes, with one scale, and optionally one zero point, for every `group` columns of a row:
+ *     W[r][c] = T((code[r][c] - zero[r][c / group]) * scale[r][c / group])
+ * the number of type T nearest to the product (ties to even).  These numbers are what the products
+ * below multiply, exactly as gemm_bf16_f32acc / gemm_f16_f32acc would multiply a stored W: products
+ * and sums in FP32.
+ *   codes    two to a byte along each row, even columns in the low half; ld_codes bytes from row to
+ *            row, at least (cols + 1) / 2; in an odd row's last byte the high half is not read
+ *   scales   T bit patterns, ld_scales elements from row to row, at least ceil(cols / group); finite,
+ *            or NaN (then the whole group stands for NaN; so does an infinite scale)
+ *   zeros    one byte (0 .. 255) per group, ld_zeros bytes from row to row, at least
+ *            ceil(cols / group); NULL: 8 everywhere, and ld_zeros is ignored
+ *   group    32, 64 or 128; the last group of a row may be partly filled */
+typedef struct {
+    uint8_t *codes;
+    int64_t ld_codes;
+    void *scales;
+    int64_t ld_scales;
+    uint8_t *zeros;
+    int64_t ld_zeros;
+    int group;
+} gemm_w4_t;
+
+/* gemm_bf16_w4_quantize / gemm_f16_w4_quantize: rounds W (rows x cols, row-major, T bit patterns,
+ * leading dimension ldw) to 4 bits; writes Q's codes, scales and, if it has them, zero points.
+ *   without zero points:  scale = T(max |W| / 7),  code = round(W / scale) + 8
+ *   with zero points:     scale = T((max - min) / 15) over the group's values and 0,
+ *                         zero = round(-min / scale),  code = round(W / scale) + zero
+ * each held in 0 .. 15, rounding to nearest with ties to even, divisions in FP32.  A scale of 0 gives
+ * codes and zero point 8; a group with an infinity or a NaN gets a NaN scale.
+ * gemm_bf16_w4_dequantize / gemm_f16_w4_dequantize: writes the matrix Q stands for.
+ * Errors: GEMM_ERR_INVALID_VALUE for negative or too large extents (> INT_MAX), a leading dimension
+ * too small, an unknown group, a null pointer for a non-empty matrix, or a 16-bit pointer at an odd
+ * address; GEMM_ERR_UNSUPPORTED_DEVICE and GEMM_ERR_LAUNCH as for the products. */
+gemm_status_t gemm_bf16_w4_quantize(int64_t rows, int64_t cols, const uint16_t *W, int64_t ldw,
+                                    const gemm_w4_t *Q, hipStream_t stream);
+gemm_status_t gemm_f16_w4_quantize(int64_t rows, int64_t cols, const uint16_t *W, int64_t ldw,
+                                   const gemm_w4_t *Q, hipStream_t stream);
+gemm_status_t gemm_bf16_w4_dequantize(int64_t rows, int64_t cols, const gemm_w4_t *Q, uint16_t *W,
+                                      int64_t ldw, hipStream_t stream);
+gemm_status_t gemm_f16_w4_dequantize(int64_t rows, int64_t cols, const gemm_w4_t *Q, uint16_t *W,
+                                     int64_t ldw, hipStream_t stream);
+
+/* gemm_bf16_w4 / gemm_f16_w4: C = act(alpha * A.B + beta * C + bias), B in 4 bits.  A is M x K,
+ * row-major, T; C is M x N, row-major, float or 16-bit per the epilogue's out_type (any of the three
+ * for either T).  epilogue == NULL: C = A.B in FP32.  B is K x N:
+ *   order_b == GEMM_COL_MAJOR  W holds B^T, N rows of K columns: a layer's forward product x . W^T
+ *   order_b == GEMM_ROW_MAJOR  W holds B, K rows of N columns: the layer's input gradient dy . W
+ * Any M, N, K and alignment; K == 0 gives act(beta * C + bias).  Few rows are decoded inside the
+ * product; for many, W is first written as T into the workspace, from which the 16-bit direct-copy
+ * kernels run (gemm_last_kernel() names them).  Results are deterministic.
+ * workspace: device memory, 16-byte aligned, not overlapping A, C or W, used only if workspace_bytes >=
+ * gemm_w4_workspace_size(...) and that is not 0; without it every problem runs on the kernel for few
+ * rows.  Calls that share one workspace must not run concurrently.
+ * Errors: GEMM_ERR_INVALID_VALUE as for the other products and gemm_w4_quantize, and for an unknown order,
+ * activation or output type, a bias not 4-byte aligned, a C not aligned to its element, or a workspace
+ * not 16-byte aligned. */
+size_t gemm_w4_workspace_size(int64_t M, int64_t N, int64_t K, gemm_order_t order_b);
+gemm_status_t gemm_bf16_w4(int64_t M, int64_t N, int64_t K, const uint16_t *A, int64_t lda,
+                           const gemm_w4_t *W, gemm_order_t order_b, void *C, int64_t ldc,
+                           const gemm_epilogue_t *epilogue, void *workspace, size_t workspace_bytes,
+                           hipStream_t stream);
+gemm_status_t gemm_f16_w4(int64_t M, int64_t N, int64_t K, const uint16_t *A, int64_t lda,
+                          const gemm_w4_t *W, gemm_order_t order_b, void *C, int64_t ldc,
+                          const gemm_epilogue_t *epilogue, void *workspace, size_t workspace_bytes,
+                          hipStream_t stream);
+
+/* ---- Low-bit operands: activations kept in 8 bits for the backward pass -------------------
+ * A layer's weight gradient dW = dY^T . X needs the layer's input X again; kept as 16-bit numbers
+ * these inputs are most of a training step's memory.  A gemm_x8_t holds a rows x cols matrix (tokens x
+ * features) as E4M3 codes (the format of GEMM_FP8_E4M3) with one exponent byte for every 32 columns
+ * of a row:
+ *     X[r][c] = e4m3(code[r][c]) * 2^(exponent[r][c / 32] - 127)
+ *   codes      one byte each, ld_codes from row to row, at least cols
+ *   exponents  1 .. 254, ld_exponents bytes from row to row, at least ceil(cols / 32) */
+typedef struct {
+    uint8_t *codes;
+    int64_t ld_codes;
+    uint8_t *exponents;
+    int64_t ld_exponents;
+} gemm_x8_t;
+
+/* gemm_bf16_x8_quantize / gemm_f16_x8_quantize: rounds X (rows x cols, row-major, T) to 8 bits.  A
+ * group's exponent is the smallest at which its largest finite magnitude is within E4M3's 448, but at
+ * least -117 (bf16) or -15 (fp16); a value is rounded to nearest, ties to even (an error of at most
+ * 2^-4 of it, or of half of E4M3's smallest step, 2^-10 2^exponent).  Every value that results is a
+ * number of type T, for which magnitudes over 240 * 2^120 (bf16) or 240 * 2^8 (fp16) are held at that.
+ * Infinities and NaN become NaN and do not count for the exponent.
+ * gemm_bf16_x8_dequantize / gemm_f16_x8_dequantize: the matrix Q stands for, as T (exact for exponents
+ * that the same T's quantize wrote, else rounded to nearest).
+ * gemm_bf16_x8_wgrad / gemm_f16_x8_wgrad: C = alpha * dY^T . X + beta * C (N x K, row-major, float or
+ * 16-bit per out_type): dY is T x N tokens by output features, row-major, type T, X is T x K in 8 bits.
+ * Products and sums are FP32; beta = 1 adds to the gradient of earlier micro-batches.
+ * workspace: device memory, 16-byte aligned, of at least gemm_x8_wgrad_workspace_size(tokens, N, K)
+ * bytes, not overlapping the other operands: X's 16-bit numbers, and dY where N % 8 != 0.  Calls that
+ * share one must not run concurrently.  tokens == 0 gives beta * C.
+ * Errors: as for the 4-bit calls, and GEMM_ERR_INVALID_VALUE for a workspace that is missing or too
+ * small, and for operands whose element offsets reach 2^30 (tokens * N, tokens * K with the leading
+ * dimension of dY). */
+gemm_status_t gemm_bf16_x8_quantize(int64_t rows, int64_t cols, const uint16_t *X, int64_t ldx,
+                                    const gemm_x8_t *Q, hipStream_t stream);
+gemm_status_t gemm_f16_x8_quantize(int64_t rows, int64_t cols, const uint16_t *X, int64_t ldx,
+                                   const gemm_x8_t *Q, hipStream_t stream);
+gemm_status_t gemm_bf16_x8_dequantize(int64_t rows, int64_t cols, const gemm_x8_t *Q, uint16_t *X,
+                                      int64_t ldx, hipStream_t stream);
+gemm_status_t gemm_f16_x8_dequantize(int64_t rows, int64_t cols, const gemm_x8_t *Q, uint16_t *X,
+                                     int64_t ldx, hipStream_t stream);
+size_t gemm_x8_wgrad_workspace_size(int64_t tokens, int64_t N, int64_t K);
+gemm_status_t gemm_bf16_x8_wgrad(int64_t tokens, int64_t N, int64_t K, const uint16_t *dY, int64_t lddy,
+                                 const gemm_x8_t *X, void *C, int64_t ldc, float alpha, float beta,
+                                 gemm_out_t out_type, void *workspace, size_t workspace_bytes,
+                                 hipStream_t stream);
+gemm_status_t gemm_f16_x8_wgrad(int64_t tokens, int64_t N, int64_t K, const uint16_t *dY, int64_t lddy,
+                                const gemm_x8_t *X, void *C, int64_t ldc, float alpha, float beta,
+                                gemm_out_t out_type, void *workspace, size_t workspace_bytes,
+                                hipStream_t stream);
 
 #ifdef __cplusplus
 }
