@@ -28,14 +28,23 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kWaves = 8;
 
-// 8 elements of a row of A from k on; zero past K
-__device__ __forceinline__ uint4 load_a(const uint16_t* row, int k, int K, bool whole) {
-    if (whole || k + 8 <= K) return load16(row + k);
-    uint32_t v[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = k + e < K ? row[k + e] : 0u;
-    return make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+// The 16 bytes v shifted down by n bytes (n >= 0; 16 and more leave nothing), zero from above.  By whole
+// words, then by bytes within them: selections, no branch on the lane.
+__device__ __forceinline__ uint4 shift_down(uint4 v, int n) {
+    if (n & 8) v = make_uint4(v.z, v.w, 0u, 0u);
+    if (n & 4) v = make_uint4(v.y, v.z, v.w, 0u);
+    v = make_uint4(__builtin_amdgcn_alignbyte(v.y, v.x, n & 3), __builtin_amdgcn_alignbyte(v.z, v.y, n & 3),
+                   __builtin_amdgcn_alignbyte(v.w, v.z, n & 3), __builtin_amdgcn_alignbyte(0u, v.w, n & 3));
+    return n < 16 ? v : make_uint4(0u, 0u, 0u, 0u);
 }
+
+// The end of a row of n >= 16 bytes: where the 16 bytes from byte i on would run past it, the row's last
+// 16 are loaded instead (load_end), and shifted into place once they are there (shift_down by end_shift).
+__device__ __forceinline__ uint4 load_end(const uint8_t* row, int64_t i, int64_t n) {
+    const u32x4_ub v = *reinterpret_cast<const u32x4_ub*>(row + min(i, n - 16));
+    return make_uint4(v.x, v.y, v.z, v.w);
+}
+__device__ __forceinline__ int end_shift(int64_t i, int64_t n) { return (int)max((int64_t)0, min(i - (n - 16), (int64_t)16)); }
 
 // keep the first n of 8 packed elements (n may be negative or over 8)
 __device__ __forceinline__ uint4 keep_first(uint4 v, int n) {
@@ -45,12 +54,216 @@ __device__ __forceinline__ uint4 keep_first(uint4 v, int n) {
     return v;
 }
 
-template <bool F16, int FM, int FN, bool TR>
+// Four rows of a column of C through the epilogue.
+__device__ __forceinline__ void store_column(const W4Problem& p, const f32x4& sum, int row, int col) {
+    const float bias = p.e.bias == nullptr ? 0.f : p.e.bias[col];
+    const int64_t off = (int64_t)row * p.ldc + col;
+    float old[4] = {0.f, 0.f, 0.f, 0.f};
+    if (p.e.beta != 0.f) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (row + r < p.M) old[r] = epi_load(p.e, p.C, off + r * p.ldc);
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        if (row + r >= p.M) break;
+        epi_store(p.e, p.C, off + r * p.ldc, epi_apply(p.e, sum[r], old[r], bias));
+    }
+}
+
+// ---- at most 16 rows, x . W^T ---------------------------------------------------------------
+// Bound by the bytes of W, at the smallest sizes by latency, and in between by the number of load
+// instructions a CU can issue: so W's codes are all that the loop loads when it can be.
+//  * A workgroup owns 16 FN columns; its NW wavefronts take steps of 128 k in turn.  Latency is hidden by
+//    the other wavefronts of the CU, not by loading further ahead: two or four steps in flight per
+//    wavefront were slower everywhere (1 x 4096 x 4096 4.5 -> 4.9 and 5.2 us, 1 x 11008 x 4096 7.7 -> 8.7
+//    and 9.5, 16 x 11008 x 4096 10.8 -> 12.8), as all of a CU's data then arrives before any is decoded.
+//  * Scales and zero points of the workgroup's columns are staged in LDS first, one word a group, while
+//    the first codes are on their way (two scattered loads a step otherwise).
+//  * XL: so is A, where it is small (a load of A from L2 carries 16 bytes for each of 16 rows, whether
+//    or not there are as many); else A's fragments come from L2 with the codes.
+//  * Loads are buffer loads, a per-lane offset fixed for the whole kernel plus a scalar one.  Lanes of
+//    rows past M (columns past N) read past the buffer's end, which returns zero and moves nothing.
+constexpr int kBufWord3 = 0x00020000;            // 32-bit unformatted data, no swizzle
+constexpr unsigned kPastEnd = 0x80000000u;       // an offset past any of the buffers below (the host checks)
+
+__device__ __forceinline__ uint4 buf16(__amdgpu_buffer_rsrc_t r, unsigned voff, int soff) {
+    return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, voff, soff, 0));
+}
+
+// words between the groups of two columns in LDS: odd, so that 16 columns fall on 16 banks
+__host__ __device__ constexpr int few_stride(int groups) { return groups | 1; }
+// bytes between two rows of A in LDS: the 16 rows read together 16 bytes apart in the banks
+__host__ __device__ constexpr int few_row(int K) { return (K * 2 + 255) / 256 * 256 + 16; }
+
+template <bool F16, int FN, int NW, bool XL>
+__global__ __launch_bounds__(64 * NW) void k_w4_few(W4Problem p) {
+    constexpr int BN = 16 * FN, KU = 128, T = 64 * NW;
+    extern __shared__ __align__(16) unsigned char lds[];
+    uint32_t* sz = reinterpret_cast<uint32_t*>(lds);                 // [BN][few_stride]: scale | zero << 16
+
+    const int n0 = blockIdx.x * BN, tid = threadIdx.x;
+    const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int li = lane & 15, lq = lane >> 4;
+    const int K = p.K, gs = p.w.gshift, cols = min(BN, p.N - n0);
+    const int kb = (K + 1) / 2, groups = ((K - 1) >> gs) + 1, gw = few_stride(groups);
+    unsigned char* xl = lds + (BN * gw * 4 + 15) / 16 * 16;
+    // (each buffer ends with its last row's last element)
+    const int ea = (int)(((int64_t)(p.M - 1) * p.lda + K) * 2), ec = (int)((int64_t)(cols - 1) * p.w.ld + kb);
+    const uint8_t* codes = p.w.codes + (int64_t)n0 * p.w.ld;
+    auto buffer = [](const void* base, int bytes) {
+        return __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, bytes, kBufWord3);
+    };
+    // this lane's 32 k of a step start at 32 lq
+    const unsigned avoff = li < p.M ? (unsigned)(li * (int)p.lda * 2 + 64 * lq) : kPastEnd;
+    unsigned cvoff[FN];
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+        cvoff[j] = 16 * j + li < cols ? (unsigned)((16 * j + li) * (int)p.w.ld + 16 * lq) : kPastEnd;
+
+    uint4 c[FN], a[4];
+    const int whole = K / KU;
+    const __amdgpu_buffer_rsrc_t rc = buffer(codes, ec), ra = buffer(p.A, ea);
+    auto load = [&](int u) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j) c[j] = buf16(rc, cvoff[j], u * 64);
+        if constexpr (!XL) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) a[t] = buf16(ra, avoff + 16 * t, u * 256);
+        }
+    };
+    if (wave < whole) load(wave);
+
+    // the scales and zero points of this workgroup's columns, and A
+    for (int i = tid; i < cols * groups; i += T) {
+        const int nn = i / groups, g = i - nn * groups;
+        const uint32_t sc = p.w.scales[(n0 + nn) * p.w.lds + g];
+        const uint32_t zz = p.w.zeros != nullptr ? p.w.zeros[(n0 + nn) * p.w.ldz + g] : 8u;
+        sz[nn * gw + g] = sc | zz << 16;
+    }
+    const int xrow = few_row(K);
+    if constexpr (XL) {
+        const int chunks = (K + 7) / 8;
+        for (int m = 0; m < p.M; ++m) {
+            const uint8_t* row = reinterpret_cast<const uint8_t*>(p.A + (int64_t)m * p.lda);
+            for (int i = tid; i < chunks; i += T)
+                *reinterpret_cast<uint4*>(xl + m * xrow + 16 * i) =
+                    shift_down(load_end(row, 16 * (int64_t)i, 2 * (int64_t)K), end_shift(16 * (int64_t)i, 2 * (int64_t)K));
+        }
+    }
+    __syncthreads();
+
+    f32x4 acc[FN];
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    // columns past N take the last one's scales: what they give is never stored
+    const uint32_t* szl[FN];
+#pragma unroll
+    for (int j = 0; j < FN; ++j) szl[j] = sz + min(16 * j + li, cols - 1) * gw;
+    const unsigned char* xrd = xl + min(li, p.M - 1) * xrow;
+    // this lane's 32 k from k0 on; `last`: only the first `left` of them lie before K
+    auto multiply = [&](int k0, bool last, int left) {
+        uint4 x[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            if constexpr (XL) {
+                x[t] = *reinterpret_cast<const uint4*>(xrd + (last ? min(k0 + 8 * t, (K - 1) & ~7) : k0 + 8 * t) * 2);
+                if (last && left <= 8 * t) x[t] = make_uint4(0u, 0u, 0u, 0u);
+            } else
+                x[t] = a[t];
+        }
+        const int g = (last ? min(k0, K - 1) : k0) >> gs;
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+            const uint32_t v = szl[j][g];
+            const float sc = from16<F16>((uint16_t)v), zs = -sc * (float)(v >> 16);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                uint4 b = w4_eight<F16>((&c[j].x)[t], sc, zs);
+                if (last) b = keep_first(b, left - 8 * t);
+                acc[j] = mma_16x16x32<F16>(__builtin_bit_cast(bf16x8, x[t]), __builtin_bit_cast(bf16x8, b), acc[j]);
+            }
+        }
+    };
+    for (int u = wave; u < whole; u += NW) {            // (uniform)
+        multiply(u * KU + 32 * lq, false, 0);
+        if (u + NW < whole) load(u + NW);
+    }
+    if (K % KU != 0 && whole % NW == wave) {            // the step that K ends in (uniform)
+        const int k = whole * KU + 32 * lq;
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+            c[j] = load_end(codes + (int64_t)min(16 * j + li, cols - 1) * p.w.ld, k / 2, kb);
+        if constexpr (!XL) {
+            const uint8_t* row = reinterpret_cast<const uint8_t*>(p.A + (int64_t)min(li, p.M - 1) * p.lda);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) a[t] = load_end(row, 2 * (k + 8 * t), 2 * (int64_t)K);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) a[t] = shift_down(a[t], end_shift(2 * (k + 8 * t), 2 * (int64_t)K));
+        }
+#pragma unroll
+        for (int j = 0; j < FN; ++j) c[j] = shift_down(c[j], end_shift(k / 2, kb));
+        multiply(k, true, K - k);
+    }
+
+    // ---- the wavefronts' sums, added in their order (a thread per output); then the epilogue ----
+    __syncthreads();
+    f32x4* red = reinterpret_cast<f32x4*>(lds);                      // [NW][FN][64]
+#pragma unroll
+    for (int j = 0; j < FN; ++j) red[(wave * FN + j) * 64 + lane] = acc[j];
+    __syncthreads();
+    const float* sums = reinterpret_cast<const float*>(lds);
+    for (int i = tid; i < FN * 256; i += T) {
+        // value i: fragment i / 256, its lane (i / 4) % 64, register i % 4
+        const int row = 4 * ((i >> 6) & 3) + (i & 3), col = n0 + 16 * (i >> 8) + ((i >> 2) & 15);
+        float sum = sums[i];
+#pragma unroll
+        for (int w = 1; w < NW; ++w) sum += sums[w * FN * 256 + i];
+        if (row >= p.M || col >= p.N) continue;
+        const int64_t off = (int64_t)row * p.ldc + col;
+        const float old = p.e.beta != 0.f ? epi_load(p.e, p.C, off) : 0.f;
+        epi_store(p.e, p.C, off, epi_apply(p.e, sum, old, p.e.bias == nullptr ? 0.f : p.e.bias[col]));
+    }
+}
+
+// The wavefronts' sums, added in a fixed order ((0 + 4) + (1 + 5) + (2 + 6) + (3 + 7)), then the
+// epilogue.  col(j): the column of C that fragment j of this lane holds.
+template <int FM, int FN, typename Col>
+__device__ __forceinline__ void finish(const W4Problem& p, f32x4 (&acc)[FM][FN], f32x4 (&red)[kWaves / 2][FM][FN][64],
+                                       int wave, int lane, int m0, Col col) {
+    constexpr int H = kWaves / 2;
+    if (wave >= H) {
+#pragma unroll
+        for (int f = 0; f < FM; ++f)
+#pragma unroll
+            for (int j = 0; j < FN; ++j) red[wave - H][f][j][lane] = acc[f][j];
+    }
+    __syncthreads();
+    if (wave < H) {
+#pragma unroll
+        for (int f = 0; f < FM; ++f)
+#pragma unroll
+            for (int j = 0; j < FN; ++j) red[wave][f][j][lane] += acc[f][j];
+    }
+    __syncthreads();
+    for (int i = wave; i < FM * FN; i += kWaves) {
+        const int f = i / FN, j = i % FN;
+        f32x4 sum = red[0][f][j][lane];
+#pragma unroll
+        for (int w = 1; w < H; ++w) sum += red[w][f][j][lane];
+        const int c = col(j);
+        if (c >= p.N) continue;
+        store_column(p, sum, m0 + 16 * f + 4 * (lane >> 4), c);
+    }
+}
+
+// x . W^T.  U: 8-code instructions' worth of k per lane and step (a step is 32 U of k); RING: steps
+// whose loads are in flight; ZP: W has zero points.
+template <bool F16, int FM, int FN, int U, int RING, bool ZP>
 __global__ __launch_bounds__(64 * kWaves) void k_w4_rows(W4Problem p) {
-    static_assert(!TR || FN == 4, "two bytes of a row of W are four columns");
-    constexpr int BM = 16 * FM, BN = 16 * FN;
-    constexpr int KU = TR ? 32 : 128;               // k per wavefront and step
-    __shared__ f32x4 red[kWaves][FM][FN][64];
+    constexpr int BM = 16 * FM, BN = 16 * FN, KU = 32 * U;
+    static_assert(U == 2 || U == 4, "8 or 16 bytes of codes per load");
+    __shared__ f32x4 red[kWaves / 2][FM][FN][64];
 
     const int slabs = (p.N + BN - 1) / BN, rblocks = (p.M + BM - 1) / BM;
     int rb, slab;
@@ -60,155 +273,305 @@ __global__ __launch_bounds__(64 * kWaves) void k_w4_rows(W4Problem p) {
     const int li = lane & 15, lq = lane >> 4;
     const int K = p.K;
 
-    // rows of A past M are read as the last one: their products are never stored
+    // rows of A past M and columns past N are read as the last one: their products are never stored
     const uint16_t* arow[FM];
+    const uint8_t* crow[FN];
+    const uint16_t* srow[FN];
+    const uint8_t* zrow[FN];
 #pragma unroll
     for (int f = 0; f < FM; ++f) arow[f] = p.A + (int64_t)min(m0 + 16 * f + li, p.M - 1) * p.lda;
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+        const int64_t n = min(n0 + 16 * j + li, p.N - 1);
+        crow[j] = p.w.codes + n * p.w.ld;
+        srow[j] = p.w.scales + n * p.w.lds;
+        zrow[j] = ZP ? p.w.zeros + n * p.w.ldz : nullptr;
+    }
 
     f32x4 acc[FM][FN];
 #pragma unroll
     for (int f = 0; f < FM; ++f)
 #pragma unroll
         for (int j = 0; j < FN; ++j) acc[f][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    auto mma = [&](int f, int j, const uint4& a, const uint4& b) {
-        acc[f][j] = mma_16x16x32<F16>(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), acc[f][j]);
-    };
 
-    const int steps = (K + KU - 1) / KU;
-    if constexpr (!TR) {
-        // this lane's column of each block (the last one past N) and its row of W
-        const uint8_t* crow[FN];
-        const uint16_t* srow[FN];
-        const uint8_t* zrow[FN];
+    uint32_t c[RING + 1][FN][U];
+    uint16_t s[RING + 1][FN];
+    uint8_t z[RING + 1][FN];
+    uint4 a[RING + 1][FM][U];
+    auto load = [&](int r, int u) {                     // a step wholly inside K
+        const int k = u * KU + 8 * U * lq;
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
-            const int64_t n = min(n0 + 16 * j + li, p.N - 1);
-            crow[j] = p.w.codes + n * p.w.ld;
-            srow[j] = p.w.scales + n * p.w.lds;
-            zrow[j] = p.w.zeros == nullptr ? nullptr : p.w.zeros + n * p.w.ldz;
+            if constexpr (U == 4) {
+                const u32x4_ub v = *reinterpret_cast<const u32x4_ub*>(crow[j] + k / 2);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) c[r][j][t] = v[t];
+            } else {
+                const u32x2_ua v = *reinterpret_cast<const u32x2_ua*>(crow[j] + k / 2);
+                c[r][j][0] = v.x;
+                c[r][j][1] = v.y;
+            }
+            s[r][j] = srow[j][k >> p.w.gshift];
+            if constexpr (ZP) z[r][j] = zrow[j][k >> p.w.gshift];
         }
-        for (int u = wave; u < steps; u += kWaves) {
-            const int k = u * KU + 32 * lq;             // this lane's 32 k
-            const bool whole = (u + 1) * KU <= K;       // uniform
-            uint4 c[FN], a[FM][4];
-            float s[FN], zs[FN];
 #pragma unroll
-            for (int j = 0; j < FN; ++j) {
-                c[j] = make_uint4(0u, 0u, 0u, 0u);
-                s[j] = zs[j] = 0.f;
-                if (whole || k + 32 <= K) {
-                    const u32x4_ub v = *reinterpret_cast<const u32x4_ub*>(crow[j] + k / 2);
-                    c[j] = make_uint4(v.x, v.y, v.z, v.w);
-                } else if (k < K) {                     // the row's last bytes
-                    uint32_t* w = &c[j].x;
+        for (int f = 0; f < FM; ++f)
 #pragma unroll
-                    for (int b = 0; b < 16; ++b)
-                        if (k + 2 * b < K) w[b / 4] |= (uint32_t)crow[j][k / 2 + b] << (8 * (b % 4));
-                }
-                if (whole || k < K) {
-                    s[j] = from16<F16>(srow[j][k >> p.w.gshift]);
-                    zs[j] = -s[j] * (zrow[j] == nullptr ? 8.f : (float)zrow[j][k >> p.w.gshift]);
-                }
-            }
+            for (int t = 0; t < U; ++t) a[r][f][t] = load16(arow[f] + k + 8 * t);
+    };
+    uint4 cend[FN];
+    auto load_last = [&](int r, int u) {                // the step that K ends in
+        const int k = u * KU + 8 * U * lq, g = min(k, K - 1) >> p.w.gshift;
 #pragma unroll
-            for (int f = 0; f < FM; ++f)
+        for (int j = 0; j < FN; ++j) {
+            cend[j] = load_end(crow[j], k / 2, (K + 1) / 2);
+            s[r][j] = srow[j][g];
+            if constexpr (ZP) z[r][j] = zrow[j][g];
+        }
 #pragma unroll
-                for (int t = 0; t < 4; ++t) a[f][t] = load_a(arow[f], k + 8 * t, K, whole);
+        for (int f = 0; f < FM; ++f)
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
+            for (int t = 0; t < U; ++t)
+                a[r][f][t] = load_end(reinterpret_cast<const uint8_t*>(arow[f]), 2 * ((int64_t)k + 8 * t), 2 * (int64_t)K);
+    };
+    auto place_last = [&](int r, int u) {               // once they are there
+        const int k = u * KU + 8 * U * lq;
 #pragma unroll
-                for (int j = 0; j < FN; ++j) {
-                    uint4 b = w4_eight<F16>((&c[j].x)[t], s[j], zs[j]);
-                    if (!whole) b = keep_first(b, K - (k + 8 * t));
+        for (int j = 0; j < FN; ++j) {
+            const uint4 v = shift_down(cend[j], end_shift(k / 2, (K + 1) / 2));
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                    for (int f = 0; f < FM; ++f) mma(f, j, a[f][t], b);
-                }
+            for (int t = 0; t < U; ++t) c[r][j][t] = w[t];
+        }
+#pragma unroll
+        for (int f = 0; f < FM; ++f)
+#pragma unroll
+            for (int t = 0; t < U; ++t)
+                a[r][f][t] = shift_down(a[r][f][t], end_shift(2 * ((int64_t)k + 8 * t), 2 * (int64_t)K));
+    };
+    // `left`: k from this lane's first to K, for the last step; its other codes are replaced by zeros
+    auto multiply = [&](int r, bool last, int left) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+            const float sc = from16<F16>(s[r][j]), zs = -sc * (ZP ? (float)z[r][j] : 8.f);
+#pragma unroll
+            for (int t = 0; t < U; ++t) {
+                uint4 b = w4_eight<F16>(c[r][j][t], sc, zs);
+                if (last) b = keep_first(b, left - 8 * t);
+#pragma unroll
+                for (int f = 0; f < FM; ++f)
+                    acc[f][j] = mma_16x16x32<F16>(__builtin_bit_cast(bf16x8, a[r][f][t]), __builtin_bit_cast(bf16x8, b),
+                                                  acc[f][j]);
             }
         }
-    } else {
-        // this lane's four columns (the last ones where they lie past N)
-        const int c = min(n0 + 4 * li, (p.N - 1) & ~3), g = c >> p.w.gshift;
-        const bool two = c + 3 <= p.N;                  // both bytes exist (N odd: the last half byte does)
-        for (int u = wave; u < steps; u += kWaves) {
-            const int k = u * KU + 8 * lq;              // this lane's 8 k
-            const bool whole = (u + 1) * KU <= K;       // uniform
-            uint32_t w[8];
-            float s[8], zs[8];
-            uint4 a[FM];
+    };
+
+    // Steps u = wave, wave + 8, ...: n whole ones, and the last one of K to the wavefront whose turn it is.
+    // The ring's loads carry no branch (the compiler could not count what is in flight across one): past
+    // the end they repeat the last whole step, which nothing multiplies.
+    const int whole = K / KU, n = whole > wave ? (whole - wave + kWaves - 1) / kWaves : 0;
+    const bool mine = K % KU != 0 && whole % kWaves == wave;
+    auto step = [&](int i) { return wave + kWaves * min(i, n - 1); };
+    if (n > 0) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int64_t r = min(k + e, K - 1);
-                const uint8_t* src = p.w.codes + r * p.w.ld + c / 2;
-                w[e] = two ? (uint32_t)*reinterpret_cast<const u16_ua*>(src) : (uint32_t)*src;
-                s[e] = from16<F16>(p.w.scales[r * p.w.lds + g]);
-                zs[e] = -s[e] * (p.w.zeros == nullptr ? 8.f : (float)p.w.zeros[r * p.w.ldz + g]);
-            }
+        for (int r = 0; r < RING; ++r) load(r, step(r));
+    }
+    if (mine) {
+        load_last(RING, whole);
+        place_last(RING, whole);
+        multiply(RING, true, K - (whole * KU + 8 * U * lq));
+    }
+    for (int i = 0; i < n; i += RING) {
 #pragma unroll
-            for (int f = 0; f < FM; ++f) a[f] = load_a(arow[f], k, K, whole);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float x[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = fmaf((float)((w[e] >> (4 * j)) & 15u), s[e], zs[e]);
-                uint4 b = make_uint4(pack16<F16>(x[0], x[1]), pack16<F16>(x[2], x[3]), pack16<F16>(x[4], x[5]),
-                                     pack16<F16>(x[6], x[7]));
-                if (!whole) b = keep_first(b, K - k);
-#pragma unroll
-                for (int f = 0; f < FM; ++f) mma(f, j, a[f], b);
-            }
+        for (int r = 0; r < RING; ++r) {
+            if (i + r < n) multiply(r, false, 0);       // (uniform)
+            if (i + RING < n) load(r, step(i + RING + r));
         }
     }
 
-    // ---- the wavefronts' sums, added in their order; then the epilogue ----
+    finish<FM, FN>(p, acc, red, wave, lane, m0, [&](int j) { return n0 + 16 * j + li; });
+}
+
+// dy . W: k runs over the rows of W.
+template <bool F16, int FM>
+__global__ __launch_bounds__(64 * kWaves) void k_w4_rows_t(W4Problem p) {
+    constexpr int FN = 4, BM = 16 * FM, BN = 16 * FN, KU = 32;
+    __shared__ f32x4 red[kWaves / 2][FM][FN][64];
+
+    const int slabs = (p.N + BN - 1) / BN, rblocks = (p.M + BM - 1) / BM;
+    int rb, slab;
+    tile_coords(blockIdx.x, rblocks, slabs, rblocks, rb, slab);
+    const int n0 = slab * BN, m0 = rb * BM;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int li = lane & 15, lq = lane >> 4;
+    const int K = p.K;
+
+    const uint16_t* arow[FM];
+#pragma unroll
+    for (int f = 0; f < FM; ++f) arow[f] = p.A + (int64_t)min(m0 + 16 * f + li, p.M - 1) * p.lda;
+    f32x4 acc[FM][FN];
 #pragma unroll
     for (int f = 0; f < FM; ++f)
 #pragma unroll
-        for (int j = 0; j < FN; ++j) red[wave][f][j][lane] = acc[f][j];
-    __syncthreads();
-    for (int i = wave; i < FM * FN; i += kWaves) {
-        const int f = i / FN, j = i % FN;
-        f32x4 sum = red[0][f][j][lane];
+        for (int j = 0; j < FN; ++j) acc[f][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    // this lane's four columns (the last ones where they lie past N)
+    const int c = min(n0 + 4 * li, (p.N - 1) & ~3), g = c >> p.w.gshift;
+    const bool two = c + 3 <= p.N;                  // both bytes exist (N odd: the last half byte does)
+    const int steps = (K + KU - 1) / KU;
+    for (int u = wave; u < steps; u += kWaves) {
+        const int k = u * KU + 8 * lq;              // this lane's 8 k
+        const bool whole = (u + 1) * KU <= K;       // uniform
+        uint32_t w[8];
+        float s[8], zs[8];
+        uint4 a[FM];
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) sum += red[w][f][j][lane];
-        const int col = TR ? n0 + 4 * li + j : n0 + 16 * j + li;
-        if (col >= p.N) continue;
-        const float bias = p.e.bias == nullptr ? 0.f : p.e.bias[col];
+        for (int e = 0; e < 8; ++e) {
+            const int64_t r = min(k + e, K - 1);
+            const uint8_t* src = p.w.codes + r * p.w.ld + c / 2;
+            w[e] = two ? (uint32_t)*reinterpret_cast<const u16_ua*>(src) : (uint32_t)*src;
+            s[e] = from16<F16>(p.w.scales[r * p.w.lds + g]);
+            zs[e] = -s[e] * (p.w.zeros == nullptr ? 8.f : (float)p.w.zeros[r * p.w.ldz + g]);
+        }
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int row = m0 + 16 * f + 4 * lq + r;
-            if (row >= p.M) continue;
-            const int64_t off = (int64_t)row * p.ldc + col;
-            const float old = p.e.beta != 0.f ? epi_load(p.e, p.C, off) : 0.f;
-            epi_store(p.e, p.C, off, epi_apply(p.e, sum[r], old, bias));
+        for (int f = 0; f < FM; ++f)
+            a[f] = shift_down(load_end(reinterpret_cast<const uint8_t*>(arow[f]), 2 * (int64_t)k, 2 * (int64_t)K),
+                              end_shift(2 * (int64_t)k, 2 * (int64_t)K));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = fmaf((float)((w[e] >> (4 * j)) & 15u), s[e], zs[e]);
+            uint4 b = make_uint4(pack16<F16>(x[0], x[1]), pack16<F16>(x[2], x[3]), pack16<F16>(x[4], x[5]),
+                                 pack16<F16>(x[6], x[7]));
+            if (!whole) b = keep_first(b, K - k);
+#pragma unroll
+            for (int f = 0; f < FM; ++f)
+                acc[f][j] = mma_16x16x32<F16>(__builtin_bit_cast(bf16x8, a[f]), __builtin_bit_cast(bf16x8, b), acc[f][j]);
         }
     }
+    finish<FM, FN>(p, acc, red, wave, lane, m0, [&](int j) { return n0 + 4 * li + j; });
+}
+
+// Fewer than 32 k (rows of codes shorter than a lane's 16 bytes): a thread per element of C.
+template <bool F16>
+__global__ __launch_bounds__(256) void k_w4_short(W4Problem p) {
+    const int64_t total = (int64_t)p.M * p.N;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        const int row = (int)(i / p.N), col = (int)(i % p.N);
+        float sum = 0.f;
+        for (int k = 0; k < p.K; ++k) {
+            const int64_t r = p.tr ? k : col;
+            const int c = p.tr ? col : k, g = c >> p.w.gshift;
+            const uint32_t code = (p.w.codes[r * p.w.ld + c / 2] >> (4 * (c & 1))) & 15u;
+            const float s = from16<F16>(p.w.scales[r * p.w.lds + g]);
+            const float z = p.w.zeros == nullptr ? 8.f : (float)p.w.zeros[r * p.w.ldz + g];
+            sum = fmaf(from16<F16>(p.A[row * p.lda + k]), from16<F16>(to16<F16>(fmaf((float)code, s, -z * s))), sum);
+        }
+        const int64_t off = row * p.ldc + col;
+        const float old = p.e.beta != 0.f ? epi_load(p.e, p.C, off) : 0.f;
+        epi_store(p.e, p.C, off, epi_apply(p.e, sum, old, p.e.bias == nullptr ? 0.f : p.e.bias[col]));
+    }
+}
+
+template <typename Kernel>
+hipError_t launch_blocks(Kernel kernel, const W4Problem& p, int bm, int bn, hipStream_t stream) {
+    const int64_t blocks = (((int64_t)p.N + bn - 1) / bn) * (((int64_t)p.M + bm - 1) / bm);
+    if (blocks > INT32_MAX) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(64 * kWaves), 0, stream, p);
+    return hipGetLastError();
+}
+
+// Registers set U and RING: two wavefronts a SIMD, 256 each.
+template <bool F16, int FM, int FN>
+hipError_t launch_rows(const W4Problem& p, hipStream_t stream) {
+    constexpr int U = FM * FN >= 8 ? 2 : 4, RING = FM == 1 && FN <= 2 ? 4 : 2;
+    return p.w.zeros != nullptr ? launch_blocks(k_w4_rows<F16, FM, FN, U, RING, true>, p, 16 * FM, 16 * FN, stream)
+                                : launch_blocks(k_w4_rows<F16, FM, FN, U, RING, false>, p, 16 * FM, 16 * FN, stream);
 }
 
 template <bool F16, int FM>
 hipError_t launch_fm(const W4Problem& p, int fn, hipStream_t stream) {
-    auto go = [&](auto kernel, int bn) {
-        const int64_t blocks = (((int64_t)p.N + bn - 1) / bn) * (((int64_t)p.M + 16 * FM - 1) / (16 * FM));
-        if (blocks > INT32_MAX) return hipErrorInvalidValue;
-        hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(64 * kWaves), 0, stream, p);
-        return hipGetLastError();
-    };
-    if (p.tr) return go(k_w4_rows<F16, FM, 4, true>, 64);
-    if (fn == 4) return go(k_w4_rows<F16, FM, 4, false>, 64);
-    if (fn == 2) return go(k_w4_rows<F16, FM, 2, false>, 32);
-    return go(k_w4_rows<F16, FM, 1, false>, 16);
+    if (p.tr) return launch_blocks(k_w4_rows_t<F16, FM>, p, 16 * FM, 64, stream);
+    if (fn == 4) return launch_rows<F16, FM, 4>(p, stream);
+    if (fn == 2) return launch_rows<F16, FM, 2>(p, stream);
+    return launch_rows<F16, FM, 1>(p, stream);
+}
+
+// LDS of a workgroup of k_w4_few: scales, and A where it is staged, then the wavefronts' sums over both.
+constexpr int64_t kFewLds = 64 << 10;
+int64_t few_lds(const W4Problem& p, int fn, int nw, bool xl) {
+    const int64_t groups = ((p.K - 1) >> p.w.gshift) + 1;
+    const int64_t stage = (16 * fn * (groups | 1) * 4 + 15) / 16 * 16 + (xl ? p.M * ((int64_t)p.K * 2 + 272) : 0);
+    return std::max<int64_t>(stage, (int64_t)nw * fn * 1024);
+}
+
+// Column blocks of 16 per workgroup.  With A in LDS one: more workgroups a CU, some of which load while
+// others decode (1 x 11008 x 4096: 7.7 us against 9.4 and 9.1 with two and three).  Else the fewest columns
+// on the busiest CU, then the widest, since every workgroup reads A (16 x 11008 x 4096: three 10.8 us, one
+// 16.4, two 15.0; 16 x 4096 x 4096: one 7.7, two 9.2).  0: the staged operands do not fit.
+int few_blocks(const W4Problem& p, int cus, bool xl) {
+    if (xl) return 1;
+    int best = 0;
+    int64_t cost = INT64_MAX;
+    for (int fn = 1; fn <= 4; ++fn) {
+        if (few_lds(p, fn, 16, false) > kFewLds) break;
+        const int64_t blocks = ((int64_t)p.N + 16 * fn - 1) / (16 * fn), c = (blocks + cus - 1) / cus * fn;
+        if (c <= cost) { cost = c; best = fn; }
+    }
+    return best;
+}
+
+template <bool F16, int FN, int NW, bool XL>
+hipError_t launch_few_one(const W4Problem& p, hipStream_t stream) {
+    const int64_t blocks = ((int64_t)p.N + 16 * FN - 1) / (16 * FN);
+    hipLaunchKernelGGL((k_w4_few<F16, FN, NW, XL>), dim3((unsigned)blocks), dim3(64 * NW),
+                       (unsigned)few_lds(p, FN, NW, XL), stream, p);
+    return hipGetLastError();
+}
+
+// 16 wavefronts a workgroup, or 8 where a CU gets several workgroups or K has few steps for each.
+template <bool F16>
+hipError_t launch_few(const W4Problem& p, int fn, bool xl, int cus, hipStream_t stream) {
+    const bool wide = ((int64_t)p.N + 15) / 16 <= cus && p.K >= 64 * 128;
+    if (xl) return wide ? launch_few_one<F16, 1, 16, true>(p, stream) : launch_few_one<F16, 1, 8, true>(p, stream);
+    switch (fn) {
+        case 1: return wide ? launch_few_one<F16, 1, 16, false>(p, stream) : launch_few_one<F16, 1, 8, false>(p, stream);
+        case 2: return launch_few_one<F16, 2, 16, false>(p, stream);
+        case 3: return launch_few_one<F16, 3, 16, false>(p, stream);
+        default: return launch_few_one<F16, 4, 16, false>(p, stream);
+    }
 }
 
 template <bool F16>
 hipError_t launch_type(const W4Problem& p, int fm, int fn, hipStream_t stream) {
     if (fm == 1) return launch_fm<F16, 1>(p, fn, stream);
     if (fm == 2) return launch_fm<F16, 2>(p, fn, stream);
+    if (fm == 3) return launch_fm<F16, 3>(p, fn, stream);
     return launch_fm<F16, 4>(p, fn, stream);
 }
 
 }  // namespace
 
 hipError_t launch_w4_rows(const W4Problem& p, bool f16, int cus, hipStream_t stream, const char*& name) {
-    const int fm = p.M <= 16 ? 1 : p.M <= 32 ? 2 : 4;
+    if (p.K < 32) {
+        const int64_t blocks = ((int64_t)p.M * p.N + 255) / 256;
+        name = f16 ? "f16_w4_short" : "bf16_w4_short";
+        hipLaunchKernelGGL(f16 ? k_w4_short<true> : k_w4_short<false>, dim3((unsigned)std::min<int64_t>(blocks, 65536)),
+                           dim3(256), 0, stream, p);
+        return hipGetLastError();
+    }
+    // offsets within a block's rows that buffer loads can hold
+    const int64_t lim = (int64_t)1 << 30;
+    if (!p.tr && p.M <= 16 && 16 * p.lda < lim / 2 && 64 * p.w.ld < lim && 64 * p.w.lds < lim / 2 && 64 * p.w.ldz < lim) {
+        const bool xl = p.M <= 4 && few_lds(p, 1, 16, true) <= kFewLds;
+        const int fn = few_blocks(p, cus, xl);
+        if (fn > 0) {
+            name = f16 ? "f16_w4_few" : "bf16_w4_few";
+            return f16 ? launch_few<true>(p, fn, xl, cus, stream) : launch_few<false>(p, fn, xl, cus, stream);
+        }
+    }
+    const int fm = p.M <= 16 ? 1 : p.M <= 32 ? 2 : p.M <= 48 ? 3 : 4;
     const int64_t rblocks = ((int64_t)p.M + 16 * fm - 1) / (16 * fm);
     int fn = 4;
     while (!p.tr && fn > 1 && rblocks * ((p.N + 16 * fn - 1) / (16 * fn)) < cus) fn /= 2;

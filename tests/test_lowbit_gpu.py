@@ -148,7 +148,9 @@ def test_w4_product(dtype, tr, shape):
     M, rows, cols = shape
     for i, (group, zeros, out, pad) in enumerate([(32, True, "f32", 0), (64, False, dtype, 3), (128, True, "f32", 8)]):
         check_product(M, rows, cols, dtype, group, zeros, tr, out, 10 + i, pad)
-    assert g.gemm_last_kernel().startswith(f"{dtype}_w4_rows")
+    short = (rows if tr else cols) < 32
+    kernel = "w4_short" if short else "w4_rows_t" if tr else "w4_few" if M <= 16 else "w4_rows"
+    assert g.gemm_last_kernel() == f"{dtype}_{kernel}"
 
 
 @pytest.mark.parametrize("epi", [dict(bias=True, act="relu"), dict(bias=True, act="gelu"), dict(alpha=-0.5, beta=2.0),
