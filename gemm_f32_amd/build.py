@@ -24,7 +24,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgemm.so")
 
 SOURCES = ["api.hip", "fill.hip", "f32_ladder.hip", "f32_regblock.hip", "f32_mfma.hip", "f32_dma.hip",
-           "bf16_mfma.hip", "bf16_dma.hip", "skinny.hip", "api_lowbit.hip", "lowbit_codec.hip", "w4_rows.hip"]
+           "bf16_mfma.hip", "bf16_dma.hip", "skinny.hip", "api_lowbit.hip", "lowbit_codec.hip", "w4_rows.hip",
+           "w4_tile.hip"]
 ARCH = "gfx950"
 
 FLAGS = [
@@ -37,11 +38,11 @@ FLAGS = [
 ]
 
 
-# Per-source extra flags.  The FP32 direct-copy kernel keeps its matrix accumulators in
+# Per-source extra flags.  The FP32 direct-copy kernel and the 4-bit tile kernel keep their matrix accumulators in
 # ordinary vector registers: with the accumulation-register form the compiler rotated the
 # accumulators through register copies on every k-tile (visible in the kernel's assembly).
 _VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
-EXTRA_FLAGS = {"f32_dma.hip": _VGPR_FORM}
+EXTRA_FLAGS = {"f32_dma.hip": _VGPR_FORM, "w4_tile.hip": _VGPR_FORM}
 
 
 def hipcc() -> str:

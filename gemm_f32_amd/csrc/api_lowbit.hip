@@ -114,9 +114,9 @@ void w4_shape(int64_t N, int64_t K, int order_b, int64_t& rows, int64_t& cols) {
     cols = order_b == GEMM_COL_MAJOR ? K : N;
 }
 
-// Bytes of W as 16-bit numbers (rows of a multiple of 8), or 0 where the few-row kernel runs: too few
-// rows of A, K too short for the direct-copy kernels, or a W past their 31-bit offsets.
-size_t w4_workspace(int64_t M, int64_t N, int64_t K, int order_b) {
+// Bytes of W as 16-bit numbers (rows of a multiple of 8), or 0 where the direct-copy kernels do not take
+// the product: too few rows of A, K too short, or a W past their 31-bit offsets.
+size_t w4_decoded(int64_t M, int64_t N, int64_t K, int order_b) {
     if (M < kW4ManyRows || N <= 0 || K < 64) return 0;
     int64_t rows, cols;
     w4_shape(N, K, order_b, rows, cols);
@@ -124,6 +124,14 @@ size_t w4_workspace(int64_t M, int64_t N, int64_t K, int order_b) {
     if (order_b == GEMM_ROW_MAJOR && rows * ld * 2 >= (int64_t)1 << 31) return 0;
     if ((int64_t)64 * ld * 2 >= (int64_t)1 << 31) return 0;
     return (size_t)rows * ld * 2;
+}
+
+// The workspace of a product: W as 16-bit numbers, else the slices' sums of a K split over workgroups.
+size_t w4_workspace(int64_t M, int64_t N, int64_t K, int order_b) {
+    const size_t decoded = w4_decoded(M, N, K, order_b);
+    if (decoded > 0 || order_b == GEMM_ROW_MAJOR || M <= 16 || N <= 0 || K < 32) return decoded;
+    int cus = 0;
+    return w4_split(M, N, K, current_device(cus) ? cus : 256).bytes;
 }
 
 gemm_status_t w4_product(bool f16, int64_t M, int64_t N, int64_t K, const uint16_t* A, int64_t lda, const gemm_w4_t* W,
@@ -152,17 +160,28 @@ gemm_status_t w4_product(bool f16, int64_t M, int64_t N, int64_t K, const uint16
     Problem p{(int)M, (int)N, (int)K, A, lda, kRow, workspace, round8(cols), tr ? kRow : kCol,
               static_cast<float*>(C), ldc};
     if (K == 0) return record_call(run_epilogue_fill(p, e, C, stream), "epilogue_fill");
-    const size_t need = w4_workspace(M, N, K, order_b);
+    const size_t need = w4_decoded(M, N, K, order_b);
     const bool reach = (int64_t)64 * lda * 2 < (int64_t)1 << 31;      // the direct-copy kernels' A
     const char* name = "none";
-    if (need > 0 && workspace != nullptr && workspace_bytes >= need && reach) {
-        hipError_t err = launch_w4_dequantize(w, (int)rows, (int)cols, static_cast<uint16_t*>(workspace), round8(cols),
-                                              f16, stream);
-        if (err == hipSuccess) err = run_fused_tiles(f16 ? In::F16 : In::BF16, p, e, C, cus, stream, name);
-        return record_call(err, name);
-    }
+    hipError_t err = hipSuccess;
     const W4Problem wp{(int)M, (int)N, (int)K, A, lda, w, tr, C, ldc, e};
-    const hipError_t err = launch_w4_rows(wp, f16, cus, stream, name);
+    if (need > 0 && workspace != nullptr && workspace_bytes >= need && reach) {
+        err = launch_w4_dequantize(w, (int)rows, (int)cols, static_cast<uint16_t*>(workspace), round8(cols), f16, stream);
+        if (err == hipSuccess) err = run_fused_tiles(f16 ? In::F16 : In::BF16, p, e, C, cus, stream, name);
+    } else if (K < 32) {
+        err = launch_w4_short(wp, f16, stream, name);
+    } else if (tr) {
+        err = launch_w4_rows_t(wp, f16, stream, name);
+    } else if (w4_few_applies(wp, cus)) {
+        err = launch_w4_few(wp, f16, cus, stream, name);
+    } else {
+        W4Split sp = w4_split(M, N, K, cus);
+        if (workspace == nullptr || workspace_bytes < sp.bytes) {
+            sp.slices = 1;
+            sp.kslice = (int)K;
+        }
+        err = launch_w4_tile(wp, sp, f16, static_cast<float*>(workspace), stream, name);
+    }
     return record_call(err, name);
 }
 

@@ -59,8 +59,23 @@ hipError_t launch_x8_dequantize(const X8View& q, int rows, int cols, uint16_t* o
 // rows x cols 16-bit elements into rows of ldo elements
 hipError_t launch_copy16(const uint16_t* in, int64_t ldi, int rows, int cols, uint16_t* out, int64_t ldo,
                          hipStream_t stream);
-// The few-row kernel (w4_rows.hip): any M, N, K >= 1.
-hipError_t launch_w4_rows(const W4Problem& p, bool f16, int cus, hipStream_t stream, const char*& name);
+// The products (w4_rows.hip, w4_tile.hip); each sets the name that gemm_last_kernel() reports.
+// Fewer than 32 k: any M, N, either order.
+hipError_t launch_w4_short(const W4Problem& p, bool f16, hipStream_t stream, const char*& name);
+// x . W^T, M <= 16, K >= 32, within the offsets and LDS that w4_few_applies checks.
+bool w4_few_applies(const W4Problem& p, int cus);
+hipError_t launch_w4_few(const W4Problem& p, bool f16, int cus, hipStream_t stream, const char*& name);
+// dy . W: any M, N, K >= 32.
+hipError_t launch_w4_rows_t(const W4Problem& p, bool f16, hipStream_t stream, const char*& name);
+// x . W^T, any M, N, K >= 32; K in `slices` slices of `kslice`, whose sums (dense M x N, FP32) take `bytes` at
+// `part` (slices == 1: none).  fm, fn: 32-row blocks of a workgroup and 32-column blocks of a wavefront.
+struct W4Split {
+    int fm = 1, fn = 1, slices = 1, kslice = 0;
+    size_t bytes = 0;
+};
+W4Split w4_split(int64_t M, int64_t N, int64_t K, int cus);
+hipError_t launch_w4_tile(const W4Problem& p, const W4Split& sp, bool f16, float* part, hipStream_t stream,
+                          const char*& name);
 
 #ifdef __HIPCC__
 typedef float lb_f32x2 __attribute__((ext_vector_type(2)));
@@ -117,6 +132,32 @@ __device__ __forceinline__ uint2 x8_four(uint32_t w, float f) {
     const lb_f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false), b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
     return make_uint2(pack16<F16>(a.x * f, a.y * f), pack16<F16>(b.x * f, b.y * f));
 }
+// The 16 bytes v shifted down by n bytes (n >= 0; 16 and more leave nothing), zero from above.  By whole
+// words, then by bytes within them: selections, no branch on the lane.
+__device__ __forceinline__ uint4 shift_down(uint4 v, int n) {
+    if (n & 8) v = make_uint4(v.z, v.w, 0u, 0u);
+    if (n & 4) v = make_uint4(v.y, v.z, v.w, 0u);
+    v = make_uint4(__builtin_amdgcn_alignbyte(v.y, v.x, n & 3), __builtin_amdgcn_alignbyte(v.z, v.y, n & 3),
+                   __builtin_amdgcn_alignbyte(v.w, v.z, n & 3), __builtin_amdgcn_alignbyte(0u, v.w, n & 3));
+    return n < 16 ? v : make_uint4(0u, 0u, 0u, 0u);
+}
+
+// The end of a row of n >= 16 bytes: where the 16 bytes from byte i on would run past it, the row's last
+// 16 are loaded instead (load_end), and shifted into place once they are there (shift_down by end_shift).
+__device__ __forceinline__ uint4 load_end(const uint8_t* row, int64_t i, int64_t n) {
+    const u32x4_ub v = *reinterpret_cast<const u32x4_ub*>(row + min(i, n - 16));
+    return make_uint4(v.x, v.y, v.z, v.w);
+}
+__device__ __forceinline__ int end_shift(int64_t i, int64_t n) { return (int)max((int64_t)0, min(i - (n - 16), (int64_t)16)); }
+
+// keep the first n of 8 packed elements (n may be negative or over 8)
+__device__ __forceinline__ uint4 keep_first(uint4 v, int n) {
+    uint32_t* w = &v.x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] &= (n > 2 * i ? 0xffffu : 0u) | (n > 2 * i + 1 ? 0xffff0000u : 0u);
+    return v;
+}
+
 #endif
 
 }  // namespace gemm

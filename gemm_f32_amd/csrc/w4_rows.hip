@@ -28,32 +28,6 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kWaves = 8;
 
-// The 16 bytes v shifted down by n bytes (n >= 0; 16 and more leave nothing), zero from above.  By whole
-// words, then by bytes within them: selections, no branch on the lane.
-__device__ __forceinline__ uint4 shift_down(uint4 v, int n) {
-    if (n & 8) v = make_uint4(v.z, v.w, 0u, 0u);
-    if (n & 4) v = make_uint4(v.y, v.z, v.w, 0u);
-    v = make_uint4(__builtin_amdgcn_alignbyte(v.y, v.x, n & 3), __builtin_amdgcn_alignbyte(v.z, v.y, n & 3),
-                   __builtin_amdgcn_alignbyte(v.w, v.z, n & 3), __builtin_amdgcn_alignbyte(0u, v.w, n & 3));
-    return n < 16 ? v : make_uint4(0u, 0u, 0u, 0u);
-}
-
-// The end of a row of n >= 16 bytes: where the 16 bytes from byte i on would run past it, the row's last
-// 16 are loaded instead (load_end), and shifted into place once they are there (shift_down by end_shift).
-__device__ __forceinline__ uint4 load_end(const uint8_t* row, int64_t i, int64_t n) {
-    const u32x4_ub v = *reinterpret_cast<const u32x4_ub*>(row + min(i, n - 16));
-    return make_uint4(v.x, v.y, v.z, v.w);
-}
-__device__ __forceinline__ int end_shift(int64_t i, int64_t n) { return (int)max((int64_t)0, min(i - (n - 16), (int64_t)16)); }
-
-// keep the first n of 8 packed elements (n may be negative or over 8)
-__device__ __forceinline__ uint4 keep_first(uint4 v, int n) {
-    uint32_t* w = &v.x;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] &= (n > 2 * i ? 0xffffu : 0u) | (n > 2 * i + 1 ? 0xffff0000u : 0u);
-    return v;
-}
-
 // Four rows of a column of C through the epilogue.
 __device__ __forceinline__ void store_column(const W4Problem& p, const f32x4& sum, int row, int col) {
     const float bias = p.e.bias == nullptr ? 0.f : p.e.bias[col];
@@ -257,141 +231,6 @@ __device__ __forceinline__ void finish(const W4Problem& p, f32x4 (&acc)[FM][FN],
     }
 }
 
-// x . W^T.  U: 8-code instructions' worth of k per lane and step (a step is 32 U of k); RING: steps
-// whose loads are in flight; ZP: W has zero points.
-template <bool F16, int FM, int FN, int U, int RING, bool ZP>
-__global__ __launch_bounds__(64 * kWaves) void k_w4_rows(W4Problem p) {
-    constexpr int BM = 16 * FM, BN = 16 * FN, KU = 32 * U;
-    static_assert(U == 2 || U == 4, "8 or 16 bytes of codes per load");
-    __shared__ f32x4 red[kWaves / 2][FM][FN][64];
-
-    const int slabs = (p.N + BN - 1) / BN, rblocks = (p.M + BM - 1) / BM;
-    int rb, slab;
-    tile_coords(blockIdx.x, rblocks, slabs, rblocks, rb, slab);
-    const int n0 = slab * BN, m0 = rb * BM;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int li = lane & 15, lq = lane >> 4;
-    const int K = p.K;
-
-    // rows of A past M and columns past N are read as the last one: their products are never stored
-    const uint16_t* arow[FM];
-    const uint8_t* crow[FN];
-    const uint16_t* srow[FN];
-    const uint8_t* zrow[FN];
-#pragma unroll
-    for (int f = 0; f < FM; ++f) arow[f] = p.A + (int64_t)min(m0 + 16 * f + li, p.M - 1) * p.lda;
-#pragma unroll
-    for (int j = 0; j < FN; ++j) {
-        const int64_t n = min(n0 + 16 * j + li, p.N - 1);
-        crow[j] = p.w.codes + n * p.w.ld;
-        srow[j] = p.w.scales + n * p.w.lds;
-        zrow[j] = ZP ? p.w.zeros + n * p.w.ldz : nullptr;
-    }
-
-    f32x4 acc[FM][FN];
-#pragma unroll
-    for (int f = 0; f < FM; ++f)
-#pragma unroll
-        for (int j = 0; j < FN; ++j) acc[f][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-    uint32_t c[RING + 1][FN][U];
-    uint16_t s[RING + 1][FN];
-    uint8_t z[RING + 1][FN];
-    uint4 a[RING + 1][FM][U];
-    auto load = [&](int r, int u) {                     // a step wholly inside K
-        const int k = u * KU + 8 * U * lq;
-#pragma unroll
-        for (int j = 0; j < FN; ++j) {
-            if constexpr (U == 4) {
-                const u32x4_ub v = *reinterpret_cast<const u32x4_ub*>(crow[j] + k / 2);
-#pragma unroll
-                for (int t = 0; t < 4; ++t) c[r][j][t] = v[t];
-            } else {
-                const u32x2_ua v = *reinterpret_cast<const u32x2_ua*>(crow[j] + k / 2);
-                c[r][j][0] = v.x;
-                c[r][j][1] = v.y;
-            }
-            s[r][j] = srow[j][k >> p.w.gshift];
-            if constexpr (ZP) z[r][j] = zrow[j][k >> p.w.gshift];
-        }
-#pragma unroll
-        for (int f = 0; f < FM; ++f)
-#pragma unroll
-            for (int t = 0; t < U; ++t) a[r][f][t] = load16(arow[f] + k + 8 * t);
-    };
-    uint4 cend[FN];
-    auto load_last = [&](int r, int u) {                // the step that K ends in
-        const int k = u * KU + 8 * U * lq, g = min(k, K - 1) >> p.w.gshift;
-#pragma unroll
-        for (int j = 0; j < FN; ++j) {
-            cend[j] = load_end(crow[j], k / 2, (K + 1) / 2);
-            s[r][j] = srow[j][g];
-            if constexpr (ZP) z[r][j] = zrow[j][g];
-        }
-#pragma unroll
-        for (int f = 0; f < FM; ++f)
-#pragma unroll
-            for (int t = 0; t < U; ++t)
-                a[r][f][t] = load_end(reinterpret_cast<const uint8_t*>(arow[f]), 2 * ((int64_t)k + 8 * t), 2 * (int64_t)K);
-    };
-    auto place_last = [&](int r, int u) {               // once they are there
-        const int k = u * KU + 8 * U * lq;
-#pragma unroll
-        for (int j = 0; j < FN; ++j) {
-            const uint4 v = shift_down(cend[j], end_shift(k / 2, (K + 1) / 2));
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int t = 0; t < U; ++t) c[r][j][t] = w[t];
-        }
-#pragma unroll
-        for (int f = 0; f < FM; ++f)
-#pragma unroll
-            for (int t = 0; t < U; ++t)
-                a[r][f][t] = shift_down(a[r][f][t], end_shift(2 * ((int64_t)k + 8 * t), 2 * (int64_t)K));
-    };
-    // `left`: k from this lane's first to K, for the last step; its other codes are replaced by zeros
-    auto multiply = [&](int r, bool last, int left) {
-#pragma unroll
-        for (int j = 0; j < FN; ++j) {
-            const float sc = from16<F16>(s[r][j]), zs = -sc * (ZP ? (float)z[r][j] : 8.f);
-#pragma unroll
-            for (int t = 0; t < U; ++t) {
-                uint4 b = w4_eight<F16>(c[r][j][t], sc, zs);
-                if (last) b = keep_first(b, left - 8 * t);
-#pragma unroll
-                for (int f = 0; f < FM; ++f)
-                    acc[f][j] = mma_16x16x32<F16>(__builtin_bit_cast(bf16x8, a[r][f][t]), __builtin_bit_cast(bf16x8, b),
-                                                  acc[f][j]);
-            }
-        }
-    };
-
-    // Steps u = wave, wave + 8, ...: n whole ones, and the last one of K to the wavefront whose turn it is.
-    // The ring's loads carry no branch (the compiler could not count what is in flight across one): past
-    // the end they repeat the last whole step, which nothing multiplies.
-    const int whole = K / KU, n = whole > wave ? (whole - wave + kWaves - 1) / kWaves : 0;
-    const bool mine = K % KU != 0 && whole % kWaves == wave;
-    auto step = [&](int i) { return wave + kWaves * min(i, n - 1); };
-    if (n > 0) {
-#pragma unroll
-        for (int r = 0; r < RING; ++r) load(r, step(r));
-    }
-    if (mine) {
-        load_last(RING, whole);
-        place_last(RING, whole);
-        multiply(RING, true, K - (whole * KU + 8 * U * lq));
-    }
-    for (int i = 0; i < n; i += RING) {
-#pragma unroll
-        for (int r = 0; r < RING; ++r) {
-            if (i + r < n) multiply(r, false, 0);       // (uniform)
-            if (i + RING < n) load(r, step(i + RING + r));
-        }
-    }
-
-    finish<FM, FN>(p, acc, red, wave, lane, m0, [&](int j) { return n0 + 16 * j + li; });
-}
-
 // dy . W: k runs over the rows of W.
 template <bool F16, int FM>
 __global__ __launch_bounds__(64 * kWaves) void k_w4_rows_t(W4Problem p) {
@@ -482,22 +321,6 @@ hipError_t launch_blocks(Kernel kernel, const W4Problem& p, int bm, int bn, hipS
     return hipGetLastError();
 }
 
-// Registers set U and RING: two wavefronts a SIMD, 256 each.
-template <bool F16, int FM, int FN>
-hipError_t launch_rows(const W4Problem& p, hipStream_t stream) {
-    constexpr int U = FM * FN >= 8 ? 2 : 4, RING = FM == 1 && FN <= 2 ? 4 : 2;
-    return p.w.zeros != nullptr ? launch_blocks(k_w4_rows<F16, FM, FN, U, RING, true>, p, 16 * FM, 16 * FN, stream)
-                                : launch_blocks(k_w4_rows<F16, FM, FN, U, RING, false>, p, 16 * FM, 16 * FN, stream);
-}
-
-template <bool F16, int FM>
-hipError_t launch_fm(const W4Problem& p, int fn, hipStream_t stream) {
-    if (p.tr) return launch_blocks(k_w4_rows_t<F16, FM>, p, 16 * FM, 64, stream);
-    if (fn == 4) return launch_rows<F16, FM, 4>(p, stream);
-    if (fn == 2) return launch_rows<F16, FM, 2>(p, stream);
-    return launch_rows<F16, FM, 1>(p, stream);
-}
-
 // LDS of a workgroup of k_w4_few: scales, and A where it is staged, then the wavefronts' sums over both.
 constexpr int64_t kFewLds = 64 << 10;
 int64_t few_lds(const W4Problem& p, int fn, int nw, bool xl) {
@@ -510,6 +333,8 @@ int64_t few_lds(const W4Problem& p, int fn, int nw, bool xl) {
 // others decode (1 x 11008 x 4096: 7.7 us against 9.4 and 9.1 with two and three).  Else the fewest columns
 // on the busiest CU, then the widest, since every workgroup reads A (16 x 11008 x 4096: three 10.8 us, one
 // 16.4, two 15.0; 16 x 4096 x 4096: one 7.7, two 9.2).  0: the staged operands do not fit.
+bool few_in_lds(const W4Problem& p) { return p.M <= 4 && few_lds(p, 1, 16, true) <= kFewLds; }
+
 int few_blocks(const W4Problem& p, int cus, bool xl) {
     if (xl) return 1;
     int best = 0;
@@ -544,40 +369,39 @@ hipError_t launch_few(const W4Problem& p, int fn, bool xl, int cus, hipStream_t 
 }
 
 template <bool F16>
-hipError_t launch_type(const W4Problem& p, int fm, int fn, hipStream_t stream) {
-    if (fm == 1) return launch_fm<F16, 1>(p, fn, stream);
-    if (fm == 2) return launch_fm<F16, 2>(p, fn, stream);
-    if (fm == 3) return launch_fm<F16, 3>(p, fn, stream);
-    return launch_fm<F16, 4>(p, fn, stream);
+hipError_t launch_t(const W4Problem& p, hipStream_t stream) {
+    if (p.M <= 16) return launch_blocks(k_w4_rows_t<F16, 1>, p, 16, 64, stream);
+    if (p.M <= 32) return launch_blocks(k_w4_rows_t<F16, 2>, p, 32, 64, stream);
+    return launch_blocks(k_w4_rows_t<F16, 4>, p, 64, 64, stream);
 }
 
 }  // namespace
 
-hipError_t launch_w4_rows(const W4Problem& p, bool f16, int cus, hipStream_t stream, const char*& name) {
-    if (p.K < 32) {
-        const int64_t blocks = ((int64_t)p.M * p.N + 255) / 256;
-        name = f16 ? "f16_w4_short" : "bf16_w4_short";
-        hipLaunchKernelGGL(f16 ? k_w4_short<true> : k_w4_short<false>, dim3((unsigned)std::min<int64_t>(blocks, 65536)),
-                           dim3(256), 0, stream, p);
-        return hipGetLastError();
-    }
+bool w4_few_applies(const W4Problem& p, int cus) {
     // offsets within a block's rows that buffer loads can hold
     const int64_t lim = (int64_t)1 << 30;
-    if (!p.tr && p.M <= 16 && 16 * p.lda < lim / 2 && 64 * p.w.ld < lim && 64 * p.w.lds < lim / 2 && 64 * p.w.ldz < lim) {
-        const bool xl = p.M <= 4 && few_lds(p, 1, 16, true) <= kFewLds;
-        const int fn = few_blocks(p, cus, xl);
-        if (fn > 0) {
-            name = f16 ? "f16_w4_few" : "bf16_w4_few";
-            return f16 ? launch_few<true>(p, fn, xl, cus, stream) : launch_few<false>(p, fn, xl, cus, stream);
-        }
-    }
-    const int fm = p.M <= 16 ? 1 : p.M <= 32 ? 2 : p.M <= 48 ? 3 : 4;
-    const int64_t rblocks = ((int64_t)p.M + 16 * fm - 1) / (16 * fm);
-    int fn = 4;
-    while (!p.tr && fn > 1 && rblocks * ((p.N + 16 * fn - 1) / (16 * fn)) < cus) fn /= 2;
-    static const char* names[2][2] = {{"bf16_w4_rows", "f16_w4_rows"}, {"bf16_w4_rows_t", "f16_w4_rows_t"}};
-    name = names[p.tr ? 1 : 0][f16 ? 1 : 0];
-    return f16 ? launch_type<true>(p, fm, fn, stream) : launch_type<false>(p, fm, fn, stream);
+    return !p.tr && p.M <= 16 && p.K >= 32 && 16 * p.lda < lim / 2 && 64 * p.w.ld < lim && 64 * p.w.lds < lim / 2 &&
+           64 * p.w.ldz < lim && few_blocks(p, cus, few_in_lds(p)) > 0;
+}
+
+hipError_t launch_w4_few(const W4Problem& p, bool f16, int cus, hipStream_t stream, const char*& name) {
+    const bool xl = few_in_lds(p);
+    const int fn = few_blocks(p, cus, xl);
+    name = f16 ? "f16_w4_few" : "bf16_w4_few";
+    return f16 ? launch_few<true>(p, fn, xl, cus, stream) : launch_few<false>(p, fn, xl, cus, stream);
+}
+
+hipError_t launch_w4_short(const W4Problem& p, bool f16, hipStream_t stream, const char*& name) {
+    const int64_t blocks = ((int64_t)p.M * p.N + 255) / 256;
+    name = f16 ? "f16_w4_short" : "bf16_w4_short";
+    hipLaunchKernelGGL(f16 ? k_w4_short<true> : k_w4_short<false>, dim3((unsigned)std::min<int64_t>(blocks, 65536)),
+                       dim3(256), 0, stream, p);
+    return hipGetLastError();
+}
+
+hipError_t launch_w4_rows_t(const W4Problem& p, bool f16, hipStream_t stream, const char*& name) {
+    name = f16 ? "f16_w4_rows_t" : "bf16_w4_rows_t";
+    return f16 ? launch_t<true>(p, stream) : launch_t<false>(p, stream);
 }
 
 }  // namespace gemm

@@ -149,8 +149,28 @@ def test_w4_product(dtype, tr, shape):
     for i, (group, zeros, out, pad) in enumerate([(32, True, "f32", 0), (64, False, dtype, 3), (128, True, "f32", 8)]):
         check_product(M, rows, cols, dtype, group, zeros, tr, out, 10 + i, pad)
     short = (rows if tr else cols) < 32
-    kernel = "w4_short" if short else "w4_rows_t" if tr else "w4_few" if M <= 16 else "w4_rows"
+    kernel = "w4_short" if short else "w4_rows_t" if tr else "w4_few" if M <= 16 else "w4_tile"
     assert g.gemm_last_kernel() == f"{dtype}_{kernel}"
+
+
+@pytest.mark.parametrize("dtype", BOTH)
+def test_w4_linear_with_k_split_over_workgroups(dtype):
+    """With the workspace, few tiles of C take K in slices whose sums are added in order: the last slice
+    shorter, K odd, every output type and step of the epilogue; with a workspace too small the call runs
+    without the split."""
+    for M, rows, cols, group, out, epi in [(17, 130, 1023, 32, "f32", {}), (33, 257, 4096, 128, dtype, dict(bias=True)),
+                                           (64, 100, 2049, 64, "f32", dict(alpha=0.5, beta=-1.0, bias=True, act="gelu")),
+                                           (200, 65, 1500, 32, "f16", dict(act="relu")), (500, 33, 700, 64, "bf16", {})]:
+        check_product(M, rows, cols, dtype, group, True, False, out, 40, pad=1, workspace="own", **epi)
+        assert g.gemm_last_kernel() == f"{dtype}_w4_tile_splitk"
+    w, _ = make_w4(130, 1023, dtype, 32, False, 3)
+    x = randn(17, 1023, dtype, 4)
+    size = g.w4_workspace_size(w, 17)
+    assert size > 0 and size % (17 * 130 * 4) == 0
+    small = torch.full((size,), 0x3f, dtype=torch.uint8, device="cuda")
+    y = g.w4_linear(x, w, workspace=small[:size - 16])
+    assert g.gemm_last_kernel() == f"{dtype}_w4_tile" and (small == 0x3f).all()
+    check_close(y, *product_reference(x.cpu().double(), g.w4_dequantize(w).cpu().double(), False))
 
 
 @pytest.mark.parametrize("epi", [dict(bias=True, act="relu"), dict(bias=True, act="gelu"), dict(alpha=-0.5, beta=2.0),
@@ -172,7 +192,7 @@ def test_w4_product_of_many_rows(dtype, tr):
         check_product(M, rows, cols, dtype, 32, True, tr, out, 30, workspace="own", **epi)
         assert "_dma" in g.gemm_last_kernel()
         check_product(M, rows, cols, dtype, 32, True, tr, out, 30, workspace="none", **epi)
-        assert "w4_rows" in g.gemm_last_kernel()
+        assert g.gemm_last_kernel() == f"{dtype}_w4_rows_t" if tr else f"{dtype}_w4_tile"
 
 
 @pytest.mark.parametrize("dtype", BOTH)
