@@ -105,8 +105,10 @@ gemm_status_t x8_dequantize(bool f16, int64_t rows, int64_t cols, const gemm_x8_
 
 // ---- products on 4-bit weights ----------------------------------------------------------
 // From this many rows of A on, W is written as 16-bit numbers once and the 16-bit direct-copy kernels
-// take the product.
-constexpr int64_t kW4ManyRows = 512;
+// take the product.  x . W^T: where their 256 x 256 tiles fill the chip often enough to pay for the extra
+// pass over W (4096^3: 112 us against 114; 2048 x 4096 x 4096: the tile kernel 57 us, 84 this way).  dy . W:
+// from the first size at which the few-row kernel's decoding per 64 rows costs more.
+constexpr int64_t kW4ManyRows = 4096, kW4ManyRowsT = 128;
 
 // The stored matrix (rows x cols of W) for a product's B.
 void w4_shape(int64_t N, int64_t K, int order_b, int64_t& rows, int64_t& cols) {
@@ -117,7 +119,7 @@ void w4_shape(int64_t N, int64_t K, int order_b, int64_t& rows, int64_t& cols) {
 // Bytes of W as 16-bit numbers (rows of a multiple of 8), or 0 where the direct-copy kernels do not take
 // the product: too few rows of A, K too short, or a W past their 31-bit offsets.
 size_t w4_decoded(int64_t M, int64_t N, int64_t K, int order_b) {
-    if (M < kW4ManyRows || N <= 0 || K < 64) return 0;
+    if (M < (order_b == GEMM_ROW_MAJOR ? kW4ManyRowsT : kW4ManyRows) || N <= 0 || K < 64) return 0;
     int64_t rows, cols;
     w4_shape(N, K, order_b, rows, cols);
     const int64_t ld = round8(cols);
@@ -131,7 +133,7 @@ size_t w4_workspace(int64_t M, int64_t N, int64_t K, int order_b) {
     const size_t decoded = w4_decoded(M, N, K, order_b);
     if (decoded > 0 || order_b == GEMM_ROW_MAJOR || M <= 16 || N <= 0 || K < 32) return decoded;
     int cus = 0;
-    return w4_split(M, N, K, current_device(cus) ? cus : 256).bytes;
+    return w4_split(M, N, K, current_device(cus) ? cus : 256, true).bytes;
 }
 
 gemm_status_t w4_product(bool f16, int64_t M, int64_t N, int64_t K, const uint16_t* A, int64_t lda, const gemm_w4_t* W,
@@ -175,11 +177,8 @@ gemm_status_t w4_product(bool f16, int64_t M, int64_t N, int64_t K, const uint16
     } else if (w4_few_applies(wp, cus)) {
         err = launch_w4_few(wp, f16, cus, stream, name);
     } else {
-        W4Split sp = w4_split(M, N, K, cus);
-        if (workspace == nullptr || workspace_bytes < sp.bytes) {
-            sp.slices = 1;
-            sp.kslice = (int)K;
-        }
+        W4Split sp = w4_split(M, N, K, cus, true);
+        if (sp.slices > 1 && (workspace == nullptr || workspace_bytes < sp.bytes)) sp = w4_split(M, N, K, cus, false);
         err = launch_w4_tile(wp, sp, f16, static_cast<float*>(workspace), stream, name);
     }
     return record_call(err, name);

@@ -68,12 +68,12 @@ hipError_t launch_w4_few(const W4Problem& p, bool f16, int cus, hipStream_t stre
 // dy . W: any M, N, K >= 32.
 hipError_t launch_w4_rows_t(const W4Problem& p, bool f16, hipStream_t stream, const char*& name);
 // x . W^T, any M, N, K >= 32; K in `slices` slices of `kslice`, whose sums (dense M x N, FP32) take `bytes` at
-// `part` (slices == 1: none).  fm, fn: 32-row blocks of a workgroup and 32-column blocks of a wavefront.
+// `part` (slices == 1: none).  fm: 32-row blocks of a workgroup, wv: its wavefronts, of 32 columns each.
 struct W4Split {
-    int fm = 1, fn = 1, slices = 1, kslice = 0;
+    int fm = 1, wv = 4, slices = 1, kslice = 0;
     size_t bytes = 0;
 };
-W4Split w4_split(int64_t M, int64_t N, int64_t K, int cus);
+W4Split w4_split(int64_t M, int64_t N, int64_t K, int cus, bool workspace);
 hipError_t launch_w4_tile(const W4Problem& p, const W4Split& sp, bool f16, float* part, hipStream_t stream,
                           const char*& name);
 

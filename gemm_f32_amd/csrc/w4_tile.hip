@@ -3,19 +3,22 @@
 //
 // Between the few-row product, bound by W's bytes, and the large one, bound by matrix instructions, the
 // costs are decoding W (19 vector instructions for the 8 codes of a lane's operand, once per
-// wavefront) and moving A from L2 (once per workgroup).  So a wavefront decodes 32 FN columns of W into
-// registers, never through LDS, and multiplies each operand with 32 FM rows of A, which all wavefronts of
+// wavefront) and moving A from L2 (once per workgroup).  So a wavefront decodes 32 columns of W into
+// registers, never through LDS, and multiplies each operand with 32 FM rows of A, which all WV wavefronts of
 // the workgroup share in LDS:
-//  * v_mfma_f32_32x32x16: lane l supplies column l % 32 of a block and, of a step of 64 k, the 32
-//    consecutive k from 32 (l / 32) on: one 16-byte load of codes, one group's, the operands of four
-//    instructions.  A's lanes read the same k.
-//  * A's tile of a step (32 FM rows of 64 k, 128 bytes each) is loaded into registers a step ahead and
-//    stored to the other of two LDS buffers, one barrier a step; 16-byte chunk c of row r at
-//    c ^ (r mod 8) ^ (bit 3 of r), so that the rows read together fall on different banks.
+//  * v_mfma_f32_32x32x16: lane l supplies column l % 32 and, of a step of 128 k, the 64 consecutive k from
+//    64 (l / 32) on, the operands of eight instructions, from 32 bytes of codes; A's lanes read the same
+//    k.  The next operand is decoded between the matrix instructions of the current one (one of them keeps
+//    the matrix unit busy for 32 cycles, in which the wavefront can issue seven vector instructions).
+//  * A's tiles (a step: 32 FM rows of 128 k, 256 bytes each) are copied from memory straight into a ring of
+//    three LDS stages, two steps ahead, as are W's codes, scales and zero points into registers; one
+//    barrier a step.  16-byte chunk c of row r lies at c ^ (r mod 16), so that the rows read together fall
+//    on different banks.
 //  * K is divided among workgroups where the tiles alone would leave CUs idle (grid y): each
 //    slice's sums go to the workspace, and a second kernel adds them in slice order and applies the
 //    epilogue (deterministic).
 #include <algorithm>
+#include <cmath>
 
 #include "common.hpp"
 #include "launch.hpp"
@@ -28,20 +31,31 @@ namespace {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-constexpr int kWavesN = 4, kThreads = 64 * kWavesN, kStep = 64;
+constexpr int kStep = 128, kRing = 3;
+constexpr int kBufWord3 = 0x00020000;            // 32-bit unformatted data, no swizzle
+typedef __attribute__((address_space(3))) void lds_void;
 
-__device__ __forceinline__ int chunk_at(int row, int c) { return c ^ (row & 7) ^ ((row >> 3) & 1); }
+// 16 bytes a lane straight into LDS.  (A function of its own: with the builtin inside the kernel's lambda the
+// host pass of this compiler silently drops the kernel's launch stub.)
+__device__ __forceinline__ void copy_to_lds(__amdgpu_buffer_rsrc_t r, lds_void* dst, unsigned voff, int soff) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, dst, 16, voff, soff, 0, 0);
+}
+
+__device__ __forceinline__ int chunk_at(int row, int c) { return c ^ (row & 15); }
 
 // part != nullptr: slice blockIdx.y's sums, dense M x N, to part + blockIdx.y M N, without the epilogue.
 // vec: rows of C (of the slices' sums) allow 16-byte FP32 or 8-byte 16-bit accesses.
-template <bool F16, int FM, int FN, bool ZP>
-__global__ __launch_bounds__(kThreads, 2) void k_w4_tile(W4Problem p, int kslice, float* part, int vec) {
-    constexpr int BM = 32 * FM, BN = 32 * FN * kWavesN, ROW = 2 * kStep;     // LDS row bytes
-    constexpr int XL = BM * 8 / kThreads;                                    // 16-byte chunks of A per thread and step
-    constexpr int EP = 32 * FN + 4;                                          // epilogue: floats per staged row
-    constexpr int XBYTES = BM * ROW, EBYTES = kWavesN * 32 * EP * 4;
-    static_assert(XL >= 1 && BM * 8 % kThreads == 0, "whole chunks per thread");
-    __shared__ __align__(16) unsigned char lds[2 * XBYTES > EBYTES ? 2 * XBYTES : EBYTES];
+// G32: groups of 32 (a lane's 64 k of a step lie in two).
+// FAR: the rows of A of a workgroup span more than a buffer's 31 bits; every step is then staged through
+// registers, as the step that K ends in always is.
+template <bool F16, int FM, int WV, bool ZP, bool G32, bool FAR>
+__global__ __launch_bounds__(64 * WV, 2) void k_w4_tile(W4Problem p, int kslice, float* part, int vec) {
+    constexpr int BM = 32 * FM, BN = 32 * WV, ROW = 2 * kStep, T = 64 * WV;     // ROW: LDS row bytes
+    constexpr int EP = 32 + 4;                                               // epilogue: floats per staged row
+    constexpr int XBYTES = BM * ROW, EBYTES = WV * 32 * EP * 4, NG = G32 ? 2 : 1;
+    constexpr int COPIES = BM / 4 / WV, LOADS = COPIES + 2 + NG * (ZP ? 2 : 1);    // of a wavefront and step
+    static_assert(COPIES >= 1 && BM % (4 * WV) == 0, "whole copies per wavefront");
+    __shared__ __align__(16) unsigned char lds[kRing * XBYTES > EBYTES ? kRing * XBYTES : EBYTES];
 
     const int tiles_m = (p.M + BM - 1) / BM, tiles_n = (p.N + BN - 1) / BN;
     int tm, tn;
@@ -50,115 +64,147 @@ __global__ __launch_bounds__(kThreads, 2) void k_w4_tile(W4Problem p, int kslice
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int l32 = lane & 31, h = lane >> 5;
     const int k_begin = blockIdx.y * kslice, K = min(p.K, k_begin + kslice);
-    const int wn = n0 + wave * 32 * FN;
+    const int wn = n0 + wave * 32, gs = p.w.gshift;
 
-    // this lane's columns of W from k 32 h on, and the chunks of A that this thread stages: chunk t % 8 of
-    // rows t / 8 + 32 i.  Rows of A past M and columns past N are read as the last one: their products are
-    // never stored.
-    const uint8_t* crow[FN];
-    const uint16_t* srow[FN];
-    const uint8_t* zrow[FN];
-#pragma unroll
-    for (int j = 0; j < FN; ++j) {
-        const int64_t n = min(wn + 32 * j + l32, p.N - 1);
-        crow[j] = p.w.codes + n * p.w.ld;
-        srow[j] = p.w.scales + n * p.w.lds;
-        zrow[j] = ZP ? p.w.zeros + n * p.w.ldz : nullptr;
-    }
-    const int xc = threadIdx.x & 7, xr = threadIdx.x >> 3;
-    const uint8_t* arow[XL];
-#pragma unroll
-    for (int i = 0; i < XL; ++i)
-        arow[i] = reinterpret_cast<const uint8_t*>(p.A + (int64_t)min(m0 + xr + 32 * i, p.M - 1) * p.lda);
+    // this lane's column of W (the last one past N: its products are never stored)
+    const int64_t n = min(wn + l32, p.N - 1);
+    const uint8_t* crow = p.w.codes + n * p.w.ld;
+    const uint16_t* srow = p.w.scales + n * p.w.lds;
+    const uint8_t* zrow = ZP ? p.w.zeros + n * p.w.ldz : nullptr;
 
-    f32x16 acc[FM][FN];
+    f32x16 acc[FM];
 #pragma unroll
     for (int f = 0; f < FM; ++f)
 #pragma unroll
-        for (int j = 0; j < FN; ++j)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) acc[f][j][r] = 0.f;
+        for (int r = 0; r < 16; ++r) acc[f][r] = 0.f;
 
-    uint4 c[2][FN], x[XL];
-    uint16_t s[2][FN];
-    uint8_t z[2][FN];
-    auto load = [&](int b, int k0) {                    // a step wholly inside K
-        const int k = k0 + 32 * h, g = k >> p.w.gshift;
+    uint4 c[kRing][2];
+    uint16_t s[kRing][NG];
+    uint8_t z[kRing][NG];
+    // a wavefront copies rows 4 (COPIES wave + i) .. + 3, lane l row l / 16's chunk for position l % 16; rows
+    // past M are read as the last one
+    const int abytes = FAR ? 0 : (int)((min(p.M - m0, BM) - 1) * p.lda * 2 + 2 * (int64_t)p.K);
+    const __amdgpu_buffer_rsrc_t ra =
+        __builtin_amdgcn_make_buffer_rsrc((void*)(p.A + (int64_t)m0 * p.lda), (short)0, abytes, kBufWord3);
+    unsigned avoff[COPIES];
 #pragma unroll
-        for (int j = 0; j < FN; ++j) {
-            const u32x4_ub v = *reinterpret_cast<const u32x4_ub*>(crow[j] + k / 2);
+    for (int i = 0; i < COPIES; ++i) {
+        const int r = 4 * (COPIES * wave + i) + (lane >> 4);
+        avoff[i] = FAR ? 0u : (unsigned)(min(r, p.M - 1 - m0) * (int)p.lda * 2 + 16 * chunk_at(r, lane & 15));
+    }
+    auto load = [&](int b, int k0) {                    // a step wholly inside K
+        const int k = k0 + 64 * h;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const u32x4_ub v = *reinterpret_cast<const u32x4_ub*>(crow + k / 2 + 16 * j);
             c[b][j] = make_uint4(v.x, v.y, v.z, v.w);
-            s[b][j] = srow[j][g];
-            if constexpr (ZP) z[b][j] = zrow[j][g];
         }
 #pragma unroll
-        for (int i = 0; i < XL; ++i) x[i] = load16(arow[i] + 2 * (k0 + 8 * xc));
-    };
-    unsigned char* xst = lds + xr * ROW + 16 * chunk_at(xr, xc);             // (rows 32 apart swizzle alike)
-    auto store = [&](int b) {
+        for (int j = 0; j < NG; ++j) {
+            s[b][j] = srow[(k >> gs) + j];
+            if constexpr (ZP) z[b][j] = zrow[(k >> gs) + j];
+        }
 #pragma unroll
-        for (int i = 0; i < XL; ++i) *reinterpret_cast<uint4*>(xst + b * XBYTES + 32 * i * ROW) = x[i];
+        for (int i = 0; i < COPIES; ++i) {
+            lds_void* dst = (lds_void*)(lds + b * XBYTES + (COPIES * wave + i) * 1024);
+            copy_to_lds(ra, dst, avoff[i], 2 * k0);
+        }
     };
     auto multiply = [&](int b, bool end, int left) {    // end: only `left` of this lane's k lie before K
-        float sc[FN], zs[FN];
+        float sc[NG], zs[NG];
 #pragma unroll
-        for (int j = 0; j < FN; ++j) {
+        for (int j = 0; j < NG; ++j) {
             sc[j] = from16<F16>(s[b][j]);
             zs[j] = -sc[j] * (ZP ? (float)z[b][j] : 8.f);
         }
+        // operand t: 8 k of W, and of A's rows (read as 16-bit vectors: with that type the compiler adds no
+        // wait for the copies in flight)
+        auto decode = [&](int t) -> uint4 {
+            const uint32_t w = (&c[b][t / 4].x)[t % 4];
+            const uint4 v = w4_eight<F16>(w, sc[G32 ? t / 4 : 0], zs[G32 ? t / 4 : 0]);
+            return end ? keep_first(v, left - 8 * t) : v;
+        };
+        auto rows = [&](int t, int f) -> bf16x8 {
+            return *reinterpret_cast<const bf16x8*>(lds + b * XBYTES + (32 * f + l32) * ROW + 16 * chunk_at(l32, 8 * h + t));
+        };
+        // A's operands are read AHEAD - 1 instructions' worth ahead (an LDS read takes as long as four matrix
+        // instructions)
+        constexpr int AHEAD = FM == 1 ? 8 : FM == 2 ? 4 : 3;
+        uint4 w[2];
+        bf16x8 a[AHEAD][FM];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            uint4 a[FM];
+        for (int t = 0; t < AHEAD - 1; ++t)
+#pragma unroll
+            for (int f = 0; f < FM; ++f) a[t][f] = rows(t, f);
+        w[0] = decode(0);
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+            if (t + AHEAD - 1 < 8) {
+#pragma unroll
+                for (int f = 0; f < FM; ++f) a[(t + AHEAD - 1) % AHEAD][f] = rows(t + AHEAD - 1, f);
+            }
+            if (t < 7) w[(t + 1) & 1] = decode(t + 1);
 #pragma unroll
             for (int f = 0; f < FM; ++f)
-                a[f] = *reinterpret_cast<const uint4*>(lds + b * XBYTES + (32 * f + l32) * ROW + 16 * chunk_at(l32, 4 * h + t));
+                acc[f] = mma_32x32x16<F16>(a[t % AHEAD][f], __builtin_bit_cast(bf16x8, w[t & 1]), acc[f]);
 #pragma unroll
-            for (int j = 0; j < FN; ++j) {
-                uint4 w = w4_eight<F16>((&c[b][j].x)[t], sc[j], zs[j]);
-                if (end) w = keep_first(w, left - 8 * t);
-#pragma unroll
-                for (int f = 0; f < FM; ++f)
-                    acc[f][j] = mma_32x32x16<F16>(__builtin_bit_cast(bf16x8, a[f]), __builtin_bit_cast(bf16x8, w), acc[f][j]);
+            for (int f = 0; f < FM; ++f) {              // a matrix instruction, a read, a share of the decoding
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x002, (20 + FM - 1) / FM, 0);
             }
         }
     };
 
-    // whole steps, the next one's loads under the current one's products (past the last, the last again:
-    // no branch, so that the compiler can count the loads in flight)
-    const int n = (K - k_begin) / kStep;
-    if (n > 0) {
-        load(0, k_begin);
-        store(0);
-        __syncthreads();
-        for (int i = 0; i < n; i += 2) {
+    // Whole steps.  At the barrier of step i every wavefront has waited for its own copies of step i (those of
+    // step i + 1 may be in flight) and is done with step i - 1, whose stage then takes step i + 2.  Past the
+    // last step the last is loaded again, into a stage that nobody reads: no branch.
+    const int whole = FAR ? 0 : (K - k_begin) / kStep;
+    if (!FAR && whole > 0) {                            // uniform
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                if (b == 1 && i + 1 >= n) break;        // uniform
-                load(b ^ 1, k_begin + min(i + b + 1, n - 1) * kStep);
-                multiply(b, false, 0);
-                store(b ^ 1);
-                __syncthreads();
+        for (int r = 0; r < kRing - 1; ++r) load(r, k_begin + min(r, whole - 1) * kStep);
+        for (int i = 0; i < whole; i += kRing) {
+#pragma unroll
+            for (int r = 0; r < kRing; ++r) {
+                if (r > 0 && i + r >= whole) break;     // uniform
+                asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" :: "n"((kRing - 2) * LOADS) : "memory");
+                __builtin_amdgcn_s_barrier();
+                asm volatile("" ::: "memory");
+                load((r + kRing - 1) % kRing, k_begin + min(i + r + kRing - 1, whole - 1) * kStep);
+                multiply(r, false, 0);
             }
         }
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");      // the surplus copies land before LDS is reused
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
     }
-    // the step that K ends in: the rows' last 16 bytes, shifted into place (the host makes sure that rows
-    // have 32 k)
-    if (K - k_begin > n * kStep) {
-        const int k0 = k_begin + n * kStep, k = k0 + 32 * h, g = min(k, p.K - 1) >> p.w.gshift;
+    // The step that K ends in (FAR: every step): where the 16 bytes would run past a row's end, its last 16
+    // shifted into place (the host makes sure that rows have 32 k).  Thread t stages chunk t % 16 of rows
+    // t / 16 + T / 16 i.
+    constexpr int XL = BM * 16 / T;
+    for (int k0 = k_begin + whole * kStep; k0 < K; k0 += kStep) {
+        const int xc = threadIdx.x & 15, xr = threadIdx.x >> 4;
+        const int k = k0 + 64 * h;
         const int64_t cb = (p.K + 1) / 2, ab = 2 * (int64_t)p.K, ak = 2 * ((int64_t)k0 + 8 * xc);
+        uint4 x[XL];
 #pragma unroll
-        for (int j = 0; j < FN; ++j) {
-            c[0][j] = load_end(crow[j], k / 2, cb);
-            s[0][j] = srow[j][g];
-            if constexpr (ZP) z[0][j] = zrow[j][g];
+        for (int j = 0; j < 2; ++j) c[0][j] = load_end(crow, k / 2 + 16 * j, cb);
+#pragma unroll
+        for (int j = 0; j < NG; ++j) {
+            const int g = min(k + 32 * j, p.K - 1) >> gs;
+            s[0][j] = srow[g];
+            if constexpr (ZP) z[0][j] = zrow[g];
         }
 #pragma unroll
-        for (int i = 0; i < XL; ++i) x[i] = load_end(arow[i], ak, ab);
+        for (int i = 0; i < XL; ++i)
+            x[i] = load_end(reinterpret_cast<const uint8_t*>(p.A + (int64_t)min(m0 + xr + T / 16 * i, p.M - 1) * p.lda), ak, ab);
 #pragma unroll
-        for (int j = 0; j < FN; ++j) c[0][j] = shift_down(c[0][j], end_shift(k / 2, cb));
+        for (int j = 0; j < 2; ++j) c[0][j] = shift_down(c[0][j], end_shift(k / 2 + 16 * j, cb));
 #pragma unroll
-        for (int i = 0; i < XL; ++i) x[i] = shift_down(x[i], end_shift(ak, ab));
-        store(0);
+        for (int i = 0; i < XL; ++i) {
+            const int r = xr + T / 16 * i;
+            *reinterpret_cast<uint4*>(lds + r * ROW + 16 * chunk_at(r, xc)) = shift_down(x[i], end_shift(ak, ab));
+        }
         __syncthreads();
         multiply(0, true, p.K - k);
         __syncthreads();
@@ -169,7 +215,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_w4_tile(W4Problem p, int kslice
     const Epilogue e = split ? Epilogue{1.f, 0.f, nullptr, 0, kActNone, kOutF32} : p.e;
     void* C = split ? static_cast<void*>(part + (int64_t)blockIdx.y * p.M * p.N) : p.C;
     const int64_t ldc = split ? p.N : p.ldc;
-    constexpr int LPR = 8 * FN, RPI = 64 / LPR;          // lanes per row, rows per store
+    constexpr int LPR = 8, RPI = 64 / LPR;               // lanes per row, rows per store
     float* band = reinterpret_cast<float*>(lds) + wave * 32 * EP;
     const int cc = 4 * (lane % LPR), col = wn + cc;
     float bias[4] = {0.f, 0.f, 0.f, 0.f};
@@ -183,9 +229,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_w4_tile(W4Problem p, int kslice
         // accumulator layout: lane l, register r holds row 8 (r / 4) + 4 (l / 32) + r % 4, column l % 32
         __builtin_amdgcn_wave_barrier();
 #pragma unroll
-        for (int j = 0; j < FN; ++j)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) band[(8 * (r >> 2) + 4 * h + (r & 3)) * EP + 32 * j + l32] = acc[f][j][r];
+        for (int r = 0; r < 16; ++r) band[(8 * (r >> 2) + 4 * h + (r & 3)) * EP + l32] = acc[f][r];
         __builtin_amdgcn_wave_barrier();
 #pragma unroll 1
         for (int q = 0; q < 32 / RPI; ++q) {
@@ -218,71 +262,121 @@ __global__ __launch_bounds__(kThreads, 2) void k_w4_tile(W4Problem p, int kslice
     }
 }
 
-// C = epilogue(slab 0 + slab 1 + ...), the slabs dense M x N, added in order.
-__global__ __launch_bounds__(256) void k_w4_join(W4Problem p, const float* part, int slices) {
-    const int64_t total = (int64_t)p.M * p.N;
+// C = epilogue(slab 0 + slab 1 + ...), the slabs dense M x N, added in order: four columns a thread, the
+// slabs' loads four at a time in flight.  vec as for the tile kernel (N % 4 == 0 too).
+__global__ __launch_bounds__(256) void k_w4_join(W4Problem p, const float* part, int slices, int vec) {
+    const int64_t slab = (int64_t)p.M * p.N, groups = (p.N + 3) / 4, total = p.M * groups;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-        const int row = (int)(i / p.N), col = (int)(i % p.N);
-        float sum = part[i];
-        for (int s = 1; s < slices; ++s) sum += part[s * total + i];
+        const int row = (int)(i / groups), col = 4 * (int)(i - row * groups);
+        const float* src = part + (int64_t)row * p.N + col;
         const int64_t off = (int64_t)row * p.ldc + col;
-        const float old = p.e.beta != 0.f ? epi_load(p.e, p.C, off) : 0.f;
-        epi_store(p.e, p.C, off, epi_apply(p.e, sum, old, p.e.bias == nullptr ? 0.f : p.e.bias[col]));
+        float sum[4] = {0.f, 0.f, 0.f, 0.f}, old[4] = {0.f, 0.f, 0.f, 0.f}, y[4];
+        if (vec) {
+#pragma unroll 4
+            for (int s = 0; s < slices; ++s) {
+                const float4 v = *reinterpret_cast<const float4*>(src + s * slab);
+                sum[0] += v.x;
+                sum[1] += v.y;
+                sum[2] += v.z;
+                sum[3] += v.w;
+            }
+            if (p.e.beta != 0.f) epi_load4(p.e, p.C, off, old);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = epi_apply(p.e, sum[e], old[e], p.e.bias == nullptr ? 0.f : p.e.bias[col + e]);
+            epi_store4(p.e, p.C, off, y);
+        } else {
+            for (int e = 0; e < 4 && col + e < p.N; ++e) {
+#pragma unroll 4
+                for (int s = 0; s < slices; ++s) sum[e] += src[s * slab + e];
+                if (p.e.beta != 0.f) old[e] = epi_load(p.e, p.C, off + e);
+                epi_store(p.e, p.C, off + e, epi_apply(p.e, sum[e], old[e], p.e.bias == nullptr ? 0.f : p.e.bias[col + e]));
+            }
+        }
     }
 }
 
-template <bool F16, int FM, int FN>
+template <bool F16, int FM, int WV>
 hipError_t launch_tile(const W4Problem& p, const W4Split& sp, float* part, hipStream_t stream) {
-    constexpr int BM = 32 * FM, BN = 32 * FN * kWavesN;
+    constexpr int BM = 32 * FM, BN = 32 * WV;
     const int64_t tiles = (((int64_t)p.M + BM - 1) / BM) * (((int64_t)p.N + BN - 1) / BN);
     if (tiles > INT32_MAX) return hipErrorInvalidValue;
     const dim3 grid((unsigned)tiles, (unsigned)sp.slices);
     float* out = sp.slices > 1 ? part : nullptr;
     // 16-byte FP32 or 8-byte 16-bit groups of four columns (the slices' sums start 16-byte aligned)
     const uintptr_t align = p.e.out == kOutF32 ? 16 : 8;
-    const int vec = out != nullptr ? p.N % 4 == 0 : p.ldc % 4 == 0 && reinterpret_cast<uintptr_t>(p.C) % align == 0;
-    if (p.w.zeros != nullptr)
-        hipLaunchKernelGGL((k_w4_tile<F16, FM, FN, true>), grid, dim3(kThreads), 0, stream, p, sp.kslice, out, vec);
-    else
-        hipLaunchKernelGGL((k_w4_tile<F16, FM, FN, false>), grid, dim3(kThreads), 0, stream, p, sp.kslice, out, vec);
-    const hipError_t err = hipGetLastError();
+    const int vec_c = p.ldc % 4 == 0 && reinterpret_cast<uintptr_t>(p.C) % align == 0, vec_n = p.N % 4 == 0;
+    const int vec = out != nullptr ? vec_n : vec_c;
+    auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, grid, dim3(64 * WV), 0, stream, p, sp.kslice, out, vec);
+        return hipGetLastError();
+    };
+    const bool zp = p.w.zeros != nullptr, g32 = p.w.gshift == 5;
+    if (FM == 1 && (int64_t)BM * p.lda * 2 >= (int64_t)1 << 31)
+        return g32 ? zp ? go(k_w4_tile<F16, FM, WV, true, true, FM == 1>) : go(k_w4_tile<F16, FM, WV, false, true, FM == 1>)
+                   : zp ? go(k_w4_tile<F16, FM, WV, true, false, FM == 1>) : go(k_w4_tile<F16, FM, WV, false, false, FM == 1>);
+    const hipError_t err =
+        g32 ? zp ? go(k_w4_tile<F16, FM, WV, true, true, false>) : go(k_w4_tile<F16, FM, WV, false, true, false>)
+            : zp ? go(k_w4_tile<F16, FM, WV, true, false, false>) : go(k_w4_tile<F16, FM, WV, false, false, false>);
     if (err != hipSuccess || sp.slices == 1) return err;
-    const int64_t blocks = ((int64_t)p.M * p.N + 255) / 256;
+    const int64_t blocks = ((int64_t)p.M * ((p.N + 3) / 4) + 255) / 256;
     hipLaunchKernelGGL(k_w4_join, dim3((unsigned)std::min<int64_t>(blocks, 4096)), dim3(256), 0, stream, p, part,
-                       sp.slices);
+                       sp.slices, vec_c && vec_n);
     return hipGetLastError();
 }
 
 template <bool F16>
 hipError_t launch_type(const W4Problem& p, const W4Split& sp, float* part, hipStream_t stream) {
-    if (sp.fm == 1) return launch_tile<F16, 1, 1>(p, sp, part, stream);
-    if (sp.fm == 2) return sp.fn == 2 ? launch_tile<F16, 2, 2>(p, sp, part, stream) : launch_tile<F16, 2, 1>(p, sp, part, stream);
-    return launch_tile<F16, 4, 2>(p, sp, part, stream);
+    if (sp.fm == 1) return launch_tile<F16, 1, 4>(p, sp, part, stream);
+    if (sp.fm == 2) return launch_tile<F16, 2, 4>(p, sp, part, stream);
+    return sp.wv == 4 ? launch_tile<F16, 4, 4>(p, sp, part, stream) : launch_tile<F16, 4, 8>(p, sp, part, stream);
 }
 
 }  // namespace
 
-W4Split w4_split(int64_t M, int64_t N, int64_t K, int cus) {
-    W4Split s;
-    s.fm = M <= 32 ? 1 : M <= 64 ? 2 : 4;
-    s.fn = s.fm == 4 ? 2 : 1;
-    const int64_t bm = 32 * s.fm, bn = 128 * s.fn, tiles = ((M + bm - 1) / bm) * ((N + bn - 1) / bn);
+// Tile and K split by a time model fitted to the kernel's times at N 4096 and 11008, K 4096 and 11008, M 32
+// to 1024 (HIP events, bf16, zero points, operands rotating over three sets): a step of 128 k takes a
+// workgroup alone on its CU `alone` us, and n workgroups that share a CU `shared` n us together (the
+// tiles of 128 rows have a CU to themselves: LDS).  A split adds a second kernel (4 us) and the slices'
+// sums, written and read once each.  The model is within 15% of the times, and its choice within 8% of
+// the best one: 64 x 4096 x 4096 15.0 us (32 x 128 tiles, 4 slices; 64 x 128 unsplit 28.9), 512 x 4096 x
+// 4096 31 us (64 x 128; 128 x 256 in 4 slices 33.7), 512 x 11008 x 4096 57.7 us (128 x 256; 64 x 128 65.5).
+W4Split w4_split(int64_t M, int64_t N, int64_t K, int cus, bool workspace) {
+    static const struct { int fm, wv; double alone, shared; int per_cu; } kTiles[] = {
+        {1, 4, 0.69, 0.57, 4}, {2, 4, 0.82, 0.72, 3}, {4, 4, 1.25, 1.25, 1}, {4, 8, 1.65, 1.65, 1}};
     const int64_t steps = (K + kStep - 1) / kStep;
-    // as many slices as give every CU a workgroup, of at least four steps each
-    int64_t slices = std::max<int64_t>(1, std::min<int64_t>(cus / std::max<int64_t>(1, tiles), steps / 4));
-    const int64_t per = (steps + slices - 1) / slices;
-    slices = (steps + per - 1) / per;
-    s.kslice = (int)(per * kStep);
-    s.slices = (int)slices;
-    s.bytes = slices > 1 ? (size_t)slices * M * N * 4 : 0;
-    return s;
+    W4Split best;
+    double cost = 1e300;
+    for (const auto& t : kTiles) {
+        const int64_t bm = 32 * t.fm, bn = 32 * t.wv;
+        const double tiles = (double)((M + bm - 1) / bm) * (double)((N + bn - 1) / bn);
+        for (int64_t want = 1; want <= (workspace ? 16 : 1) && 2 * want <= std::max<int64_t>(2, steps); ++want) {
+            const int64_t per = (steps + want - 1) / want, slices = (steps + per - 1) / per;
+            // workgroups on the busiest CU: whole rounds of `per_cu`, and what is left
+            const double load = std::ceil(tiles * slices / cus), full = std::floor(load / t.per_cu) * t.per_cu;
+            const double rest = load - full;
+            const double step = full * t.shared + (rest == 0 ? 0 : rest == 1 ? t.alone : rest * t.shared);
+            double c = 3.0 + per * step;
+            if (slices > 1) c += 4.0 + 8.0 * slices * M * N / 3e6;       // us: bytes at 3 TB/s
+            if (c < cost) {
+                cost = c;
+                best.fm = t.fm;
+                best.wv = t.wv;
+                best.slices = (int)slices;
+                best.kslice = (int)(per * kStep);
+                best.bytes = slices > 1 ? (size_t)slices * M * N * 4 : 0;
+            }
+        }
+    }
+    return best;
 }
 
 hipError_t launch_w4_tile(const W4Problem& p, const W4Split& sp, bool f16, float* part, hipStream_t stream,
                           const char*& name) {
     static const char* names[2][2] = {{"bf16_w4_tile", "f16_w4_tile"}, {"bf16_w4_tile_splitk", "f16_w4_tile_splitk"}};
     name = names[sp.slices > 1 ? 1 : 0][f16 ? 1 : 0];
-    return f16 ? launch_type<true>(p, sp, part, stream) : launch_type<false>(p, sp, part, stream);
+    W4Split s = sp;
+    if ((int64_t)32 * s.fm * p.lda * 2 >= (int64_t)1 << 31) s = W4Split{1, 4, 1, p.K, 0};      // FAR, without a split
+    return f16 ? launch_type<true>(p, s, part, stream) : launch_type<false>(p, s, part, stream);
 }
 
 }  // namespace gemm

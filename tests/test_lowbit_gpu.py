@@ -98,7 +98,8 @@ def test_w4_dequantize_every_code_and_zero_point(dtype):
 # (M, stored rows of W, stored columns): one element, one row, odd extents, several blocks, K shorter than a
 # group, a wavefront's step and its remainders, more rows than one block
 PRODUCTS = [(1, 1, 1), (1, 17, 64), (1, 300, 1000), (2, 64, 31), (5, 33, 129), (16, 48, 256), (17, 100, 1023),
-            (31, 130, 640), (33, 65, 127), (64, 128, 1152), (65, 50, 161), (130, 257, 383), (3, 8, 2048)]
+            (31, 130, 640), (33, 65, 127), (64, 128, 1152), (65, 50, 161), (130, 257, 383), (3, 8, 2048), (300, 400, 520),
+            (600, 300, 257)]
 
 
 def product_reference(x, wv, tr, alpha=1.0, beta=0.0, old=None, bias=None, act="none"):
@@ -158,13 +159,13 @@ def test_w4_linear_with_k_split_over_workgroups(dtype):
     """With the workspace, few tiles of C take K in slices whose sums are added in order: the last slice
     shorter, K odd, every output type and step of the epilogue; with a workspace too small the call runs
     without the split."""
-    for M, rows, cols, group, out, epi in [(17, 130, 1023, 32, "f32", {}), (33, 257, 4096, 128, dtype, dict(bias=True)),
+    for M, rows, cols, group, out, epi in [(17, 130, 2051, 32, "f32", {}), (33, 257, 4096, 128, dtype, dict(bias=True)),
                                            (64, 100, 2049, 64, "f32", dict(alpha=0.5, beta=-1.0, bias=True, act="gelu")),
-                                           (200, 65, 1500, 32, "f16", dict(act="relu")), (500, 33, 700, 64, "bf16", {})]:
+                                           (200, 65, 1900, 32, "f16", dict(act="relu")), (500, 33, 4001, 64, "bf16", {})]:
         check_product(M, rows, cols, dtype, group, True, False, out, 40, pad=1, workspace="own", **epi)
-        assert g.gemm_last_kernel() == f"{dtype}_w4_tile_splitk"
-    w, _ = make_w4(130, 1023, dtype, 32, False, 3)
-    x = randn(17, 1023, dtype, 4)
+        assert g.gemm_last_kernel() == f"{dtype}_w4_tile_splitk", (M, rows, cols)
+    w, _ = make_w4(130, 2051, dtype, 32, False, 3)
+    x = randn(17, 2051, dtype, 4)
     size = g.w4_workspace_size(w, 17)
     assert size > 0 and size % (17 * 130 * 4) == 0
     small = torch.full((size,), 0x3f, dtype=torch.uint8, device="cuda")
@@ -188,7 +189,8 @@ def test_w4_product_of_many_rows(dtype, tr):
     """From the row count on at which W is written as 16-bit numbers first, with and without the
     workspace; odd extents, so that rows of the workspace are padded."""
     for M, rows, cols, out, epi in [(600, 130, 200, "f32", {}), (520, 257, 131, dtype, dict(alpha=0.5, beta=1.0)),
-                                    (700, 264, 1030, "f16", {}), (513, 1001, 77, "bf16", dict(beta=-1.0))]:
+                                    (700, 264, 1030, "f16", {}), (128, 1001, 77, "bf16", dict(beta=-1.0))]:
+        M += 0 if tr else 3968
         check_product(M, rows, cols, dtype, 32, True, tr, out, 30, workspace="own", **epi)
         assert "_dma" in g.gemm_last_kernel()
         check_product(M, rows, cols, dtype, 32, True, tr, out, 30, workspace="none", **epi)
@@ -198,7 +200,7 @@ def test_w4_product_of_many_rows(dtype, tr):
 @pytest.mark.parametrize("dtype", BOTH)
 def test_w4_linear_of_many_rows_with_bias_and_activation(dtype):
     for act in ("none", "relu", "gelu"):
-        check_product(560, 300, 264, dtype, 128, False, False, dtype, 31, workspace="own", bias=True, act=act)
+        check_product(4100, 300, 264, dtype, 128, False, False, dtype, 31, workspace="own", bias=True, act=act)
         assert "_dma" in g.gemm_last_kernel()
 
 
