@@ -104,36 +104,35 @@ gemm_status_t x8_dequantize(bool f16, int64_t rows, int64_t cols, const gemm_x8_
 }
 
 // ---- products on 4-bit weights ----------------------------------------------------------
-// From this many rows of A on, W is written as 16-bit numbers once and the 16-bit direct-copy kernels
-// take the product.  x . W^T: where their 256 x 256 tiles fill the chip often enough to pay for the extra
-// pass over W (4096^3: 112 us against 114; 2048 x 4096 x 4096: the tile kernel 57 us, 84 this way).  dy . W:
-// from the first size at which the few-row kernel's decoding per 64 rows costs more.
-constexpr int64_t kW4ManyRows = 4096, kW4ManyRowsT = 128;
-
 // The stored matrix (rows x cols of W) for a product's B.
 void w4_shape(int64_t N, int64_t K, int order_b, int64_t& rows, int64_t& cols) {
     rows = order_b == GEMM_COL_MAJOR ? N : K;
     cols = order_b == GEMM_COL_MAJOR ? K : N;
 }
 
-// Bytes of W as 16-bit numbers (rows of a multiple of 8), or 0 where the direct-copy kernels do not take
-// the product: too few rows of A, K too short, or a W past their 31-bit offsets.
-size_t w4_decoded(int64_t M, int64_t N, int64_t K, int order_b) {
-    if (M < (order_b == GEMM_ROW_MAJOR ? kW4ManyRowsT : kW4ManyRows) || N <= 0 || K < 64) return 0;
+// Bytes of W as 16-bit numbers (rows of a multiple of 8) where writing them and running the 16-bit
+// direct-copy kernels is the faster way by the time model, else 0: so too where those kernels do not take the
+// product (K too short, a W past their 31-bit offsets).
+size_t w4_decoded(int64_t M, int64_t N, int64_t K, int order_b, int cus) {
+    if (M < 256 || N <= 0 || K < 64) return 0;
+    const bool tr = order_b == GEMM_ROW_MAJOR;
     int64_t rows, cols;
     w4_shape(N, K, order_b, rows, cols);
     const int64_t ld = round8(cols);
-    if (order_b == GEMM_ROW_MAJOR && rows * ld * 2 >= (int64_t)1 << 31) return 0;
+    if (tr && rows * ld * 2 >= (int64_t)1 << 31) return 0;
     if ((int64_t)64 * ld * 2 >= (int64_t)1 << 31) return 0;
+    if ((!tr || N >= 32) && w4_split(M, N, K, tr, cus, true).us <= w4_decoded_us(M, N, K, cus)) return 0;
     return (size_t)rows * ld * 2;
 }
 
 // The workspace of a product: W as 16-bit numbers, else the slices' sums of a K split over workgroups.
 size_t w4_workspace(int64_t M, int64_t N, int64_t K, int order_b) {
-    const size_t decoded = w4_decoded(M, N, K, order_b);
-    if (decoded > 0 || order_b == GEMM_ROW_MAJOR || M <= 16 || N <= 0 || K < 32) return decoded;
     int cus = 0;
-    return w4_split(M, N, K, current_device(cus) ? cus : 256, true).bytes;
+    if (!current_device(cus)) cus = 256;
+    const size_t decoded = w4_decoded(M, N, K, order_b, cus);
+    const bool tr = order_b == GEMM_ROW_MAJOR;
+    if (decoded > 0 || M <= (tr ? 0 : 16) || N < (tr ? 32 : 1) || K < 32) return decoded;
+    return w4_split(M, N, K, tr, cus, true).bytes;
 }
 
 gemm_status_t w4_product(bool f16, int64_t M, int64_t N, int64_t K, const uint16_t* A, int64_t lda, const gemm_w4_t* W,
@@ -162,7 +161,7 @@ gemm_status_t w4_product(bool f16, int64_t M, int64_t N, int64_t K, const uint16
     Problem p{(int)M, (int)N, (int)K, A, lda, kRow, workspace, round8(cols), tr ? kRow : kCol,
               static_cast<float*>(C), ldc};
     if (K == 0) return record_call(run_epilogue_fill(p, e, C, stream), "epilogue_fill");
-    const size_t need = w4_decoded(M, N, K, order_b);
+    const size_t need = w4_decoded(M, N, K, order_b, cus);
     const bool reach = (int64_t)64 * lda * 2 < (int64_t)1 << 31;      // the direct-copy kernels' A
     const char* name = "none";
     hipError_t err = hipSuccess;
@@ -170,15 +169,13 @@ gemm_status_t w4_product(bool f16, int64_t M, int64_t N, int64_t K, const uint16
     if (need > 0 && workspace != nullptr && workspace_bytes >= need && reach) {
         err = launch_w4_dequantize(w, (int)rows, (int)cols, static_cast<uint16_t*>(workspace), round8(cols), f16, stream);
         if (err == hipSuccess) err = run_fused_tiles(f16 ? In::F16 : In::BF16, p, e, C, cus, stream, name);
-    } else if (K < 32) {
+    } else if (K < 32 || (tr && N < 32)) {
         err = launch_w4_short(wp, f16, stream, name);
-    } else if (tr) {
-        err = launch_w4_rows_t(wp, f16, stream, name);
     } else if (w4_few_applies(wp, cus)) {
         err = launch_w4_few(wp, f16, cus, stream, name);
     } else {
-        W4Split sp = w4_split(M, N, K, cus, true);
-        if (sp.slices > 1 && (workspace == nullptr || workspace_bytes < sp.bytes)) sp = w4_split(M, N, K, cus, false);
+        W4Split sp = w4_split(M, N, K, tr != 0, cus, true);
+        if (sp.slices > 1 && (workspace == nullptr || workspace_bytes < sp.bytes)) sp = w4_split(M, N, K, tr != 0, cus, false);
         err = launch_w4_tile(wp, sp, f16, static_cast<float*>(workspace), stream, name);
     }
     return record_call(err, name);

@@ -60,20 +60,21 @@ hipError_t launch_x8_dequantize(const X8View& q, int rows, int cols, uint16_t* o
 hipError_t launch_copy16(const uint16_t* in, int64_t ldi, int rows, int cols, uint16_t* out, int64_t ldo,
                          hipStream_t stream);
 // The products (w4_rows.hip, w4_tile.hip); each sets the name that gemm_last_kernel() reports.
-// Fewer than 32 k: any M, N, either order.
+// Fewer than 32 k (or, dy . W, 32 columns): any M, N, either order.
 hipError_t launch_w4_short(const W4Problem& p, bool f16, hipStream_t stream, const char*& name);
 // x . W^T, M <= 16, K >= 32, within the offsets and LDS that w4_few_applies checks.
 bool w4_few_applies(const W4Problem& p, int cus);
 hipError_t launch_w4_few(const W4Problem& p, bool f16, int cus, hipStream_t stream, const char*& name);
-// dy . W: any M, N, K >= 32.
-hipError_t launch_w4_rows_t(const W4Problem& p, bool f16, hipStream_t stream, const char*& name);
-// x . W^T, any M, N, K >= 32; K in `slices` slices of `kslice`, whose sums (dense M x N, FP32) take `bytes` at
+// Either order, any M, N, K >= 32 (dy . W: N >= 32 too); K in `slices` slices of `kslice`, whose sums (dense M x N, FP32) take `bytes` at
 // `part` (slices == 1: none).  fm: 32-row blocks of a workgroup, wv: its wavefronts, of 32 columns each.
 struct W4Split {
     int fm = 1, wv = 4, slices = 1, kslice = 0;
     size_t bytes = 0;
+    double us = 0;               // the model's time
 };
-W4Split w4_split(int64_t M, int64_t N, int64_t K, int cus, bool workspace);
+W4Split w4_split(int64_t M, int64_t N, int64_t K, bool tr, int cus, bool workspace);
+// The model's time of writing W as 16-bit numbers and multiplying these.
+double w4_decoded_us(int64_t M, int64_t N, int64_t K, int cus);
 hipError_t launch_w4_tile(const W4Problem& p, const W4Split& sp, bool f16, float* part, hipStream_t stream,
                           const char*& name);
 
@@ -85,6 +86,9 @@ typedef uint32_t u32_ua __attribute__((aligned(1)));
 typedef uint16_t u16_ua __attribute__((aligned(1)));
 typedef unsigned int u32x2_ua __attribute__((ext_vector_type(2), aligned(1)));
 typedef unsigned int u32x4_ub __attribute__((ext_vector_type(4), aligned(1)));
+
+// word i (a constant) of four
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
 // two FP32 values -> two T, each to nearest, ties to even (one conversion instruction)
 template <bool F16>
@@ -152,10 +156,8 @@ __device__ __forceinline__ int end_shift(int64_t i, int64_t n) { return (int)max
 
 // keep the first n of 8 packed elements (n may be negative or over 8)
 __device__ __forceinline__ uint4 keep_first(uint4 v, int n) {
-    uint32_t* w = &v.x;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] &= (n > 2 * i ? 0xffffu : 0u) | (n > 2 * i + 1 ? 0xffff0000u : 0u);
-    return v;
+    auto mask = [n](int i) { return (n > 2 * i ? 0xffffu : 0u) | (n > 2 * i + 1 ? 0xffff0000u : 0u); };
+    return make_uint4(v.x & mask(0), v.y & mask(1), v.z & mask(2), v.w & mask(3));
 }
 
 #endif

@@ -26,25 +26,6 @@ namespace {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kWaves = 8;
-
-// Four rows of a column of C through the epilogue.
-__device__ __forceinline__ void store_column(const W4Problem& p, const f32x4& sum, int row, int col) {
-    const float bias = p.e.bias == nullptr ? 0.f : p.e.bias[col];
-    const int64_t off = (int64_t)row * p.ldc + col;
-    float old[4] = {0.f, 0.f, 0.f, 0.f};
-    if (p.e.beta != 0.f) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-            if (row + r < p.M) old[r] = epi_load(p.e, p.C, off + r * p.ldc);
-    }
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        if (row + r >= p.M) break;
-        epi_store(p.e, p.C, off + r * p.ldc, epi_apply(p.e, sum[r], old[r], bias));
-    }
-}
-
 // ---- at most 16 rows, x . W^T ---------------------------------------------------------------
 // Bound by the bytes of W, at the smallest sizes by latency, and in between by the number of load
 // instructions a CU can issue: so W's codes are all that the loop loads when it can be.
@@ -98,7 +79,10 @@ __global__ __launch_bounds__(64 * NW) void k_w4_few(W4Problem p) {
     uint4 c[FN], a[4];
     const int whole = K / KU;
     const __amdgpu_buffer_rsrc_t rc = buffer(codes, ec), ra = buffer(p.A, ea);
-    auto load = [&](int u) {
+    // (readfirstlane: otherwise the compiler takes the step for a lane's own and steps through the lanes' values of
+    // it around every load)
+    auto load = [&](int step) {
+        const int u = __builtin_amdgcn_readfirstlane(step);
 #pragma unroll
         for (int j = 0; j < FN; ++j) c[j] = buf16(rc, cvoff[j], u * 64);
         if constexpr (!XL) {
@@ -106,7 +90,10 @@ __global__ __launch_bounds__(64 * NW) void k_w4_few(W4Problem p) {
             for (int t = 0; t < 4; ++t) a[t] = buf16(ra, avoff + 16 * t, u * 256);
         }
     };
-    if (wave < whole) load(wave);
+    // (Every path to a use of the loaded registers writes them, here and in the loop: with undefined values on
+    // one path this compiler gave a decoded operand the registers of codes still to be read.  Wavefronts beyond the
+    // last step load the last, and do not use it.)
+    load(max(0, min(wave, whole - 1)));
 
     // the scales and zero points of this workgroup's columns, and A
     for (int i = tid; i < cols * groups; i += T) {
@@ -153,15 +140,15 @@ __global__ __launch_bounds__(64 * NW) void k_w4_few(W4Problem p) {
             const float sc = from16<F16>((uint16_t)v), zs = -sc * (float)(v >> 16);
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                uint4 b = w4_eight<F16>((&c[j].x)[t], sc, zs);
+                uint4 b = w4_eight<F16>(word(c[j], t), sc, zs);
                 if (last) b = keep_first(b, left - 8 * t);
                 acc[j] = mma_16x16x32<F16>(__builtin_bit_cast(bf16x8, x[t]), __builtin_bit_cast(bf16x8, b), acc[j]);
             }
         }
     };
     for (int u = wave; u < whole; u += NW) {            // (uniform)
+        if (u != wave) load(u);
         multiply(u * KU + 32 * lq, false, 0);
-        if (u + NW < whole) load(u + NW);
     }
     if (K % KU != 0 && whole % NW == wave) {            // the step that K ends in (uniform)
         const int k = whole * KU + 32 * lq;
@@ -200,99 +187,8 @@ __global__ __launch_bounds__(64 * NW) void k_w4_few(W4Problem p) {
     }
 }
 
-// The wavefronts' sums, added in a fixed order ((0 + 4) + (1 + 5) + (2 + 6) + (3 + 7)), then the
-// epilogue.  col(j): the column of C that fragment j of this lane holds.
-template <int FM, int FN, typename Col>
-__device__ __forceinline__ void finish(const W4Problem& p, f32x4 (&acc)[FM][FN], f32x4 (&red)[kWaves / 2][FM][FN][64],
-                                       int wave, int lane, int m0, Col col) {
-    constexpr int H = kWaves / 2;
-    if (wave >= H) {
-#pragma unroll
-        for (int f = 0; f < FM; ++f)
-#pragma unroll
-            for (int j = 0; j < FN; ++j) red[wave - H][f][j][lane] = acc[f][j];
-    }
-    __syncthreads();
-    if (wave < H) {
-#pragma unroll
-        for (int f = 0; f < FM; ++f)
-#pragma unroll
-            for (int j = 0; j < FN; ++j) red[wave][f][j][lane] += acc[f][j];
-    }
-    __syncthreads();
-    for (int i = wave; i < FM * FN; i += kWaves) {
-        const int f = i / FN, j = i % FN;
-        f32x4 sum = red[0][f][j][lane];
-#pragma unroll
-        for (int w = 1; w < H; ++w) sum += red[w][f][j][lane];
-        const int c = col(j);
-        if (c >= p.N) continue;
-        store_column(p, sum, m0 + 16 * f + 4 * (lane >> 4), c);
-    }
-}
-
-// dy . W: k runs over the rows of W.
-template <bool F16, int FM>
-__global__ __launch_bounds__(64 * kWaves) void k_w4_rows_t(W4Problem p) {
-    constexpr int FN = 4, BM = 16 * FM, BN = 16 * FN, KU = 32;
-    __shared__ f32x4 red[kWaves / 2][FM][FN][64];
-
-    const int slabs = (p.N + BN - 1) / BN, rblocks = (p.M + BM - 1) / BM;
-    int rb, slab;
-    tile_coords(blockIdx.x, rblocks, slabs, rblocks, rb, slab);
-    const int n0 = slab * BN, m0 = rb * BM;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int li = lane & 15, lq = lane >> 4;
-    const int K = p.K;
-
-    const uint16_t* arow[FM];
-#pragma unroll
-    for (int f = 0; f < FM; ++f) arow[f] = p.A + (int64_t)min(m0 + 16 * f + li, p.M - 1) * p.lda;
-    f32x4 acc[FM][FN];
-#pragma unroll
-    for (int f = 0; f < FM; ++f)
-#pragma unroll
-        for (int j = 0; j < FN; ++j) acc[f][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-    // this lane's four columns (the last ones where they lie past N)
-    const int c = min(n0 + 4 * li, (p.N - 1) & ~3), g = c >> p.w.gshift;
-    const bool two = c + 3 <= p.N;                  // both bytes exist (N odd: the last half byte does)
-    const int steps = (K + KU - 1) / KU;
-    for (int u = wave; u < steps; u += kWaves) {
-        const int k = u * KU + 8 * lq;              // this lane's 8 k
-        const bool whole = (u + 1) * KU <= K;       // uniform
-        uint32_t w[8];
-        float s[8], zs[8];
-        uint4 a[FM];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int64_t r = min(k + e, K - 1);
-            const uint8_t* src = p.w.codes + r * p.w.ld + c / 2;
-            w[e] = two ? (uint32_t)*reinterpret_cast<const u16_ua*>(src) : (uint32_t)*src;
-            s[e] = from16<F16>(p.w.scales[r * p.w.lds + g]);
-            zs[e] = -s[e] * (p.w.zeros == nullptr ? 8.f : (float)p.w.zeros[r * p.w.ldz + g]);
-        }
-#pragma unroll
-        for (int f = 0; f < FM; ++f)
-            a[f] = shift_down(load_end(reinterpret_cast<const uint8_t*>(arow[f]), 2 * (int64_t)k, 2 * (int64_t)K),
-                              end_shift(2 * (int64_t)k, 2 * (int64_t)K));
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float x[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = fmaf((float)((w[e] >> (4 * j)) & 15u), s[e], zs[e]);
-            uint4 b = make_uint4(pack16<F16>(x[0], x[1]), pack16<F16>(x[2], x[3]), pack16<F16>(x[4], x[5]),
-                                 pack16<F16>(x[6], x[7]));
-            if (!whole) b = keep_first(b, K - k);
-#pragma unroll
-            for (int f = 0; f < FM; ++f)
-                acc[f][j] = mma_16x16x32<F16>(__builtin_bit_cast(bf16x8, a[f]), __builtin_bit_cast(bf16x8, b), acc[f][j]);
-        }
-    }
-    finish<FM, FN>(p, acc, red, wave, lane, m0, [&](int j) { return n0 + 4 * li + j; });
-}
-
-// Fewer than 32 k (rows of codes shorter than a lane's 16 bytes): a thread per element of C.
+// Fewer than 32 k, or 32 columns of dy . W (rows of codes shorter than a lane's 16 bytes): a thread per
+// element of C.
 template <bool F16>
 __global__ __launch_bounds__(256) void k_w4_short(W4Problem p) {
     const int64_t total = (int64_t)p.M * p.N;
@@ -311,14 +207,6 @@ __global__ __launch_bounds__(256) void k_w4_short(W4Problem p) {
         const float old = p.e.beta != 0.f ? epi_load(p.e, p.C, off) : 0.f;
         epi_store(p.e, p.C, off, epi_apply(p.e, sum, old, p.e.bias == nullptr ? 0.f : p.e.bias[col]));
     }
-}
-
-template <typename Kernel>
-hipError_t launch_blocks(Kernel kernel, const W4Problem& p, int bm, int bn, hipStream_t stream) {
-    const int64_t blocks = (((int64_t)p.N + bn - 1) / bn) * (((int64_t)p.M + bm - 1) / bm);
-    if (blocks > INT32_MAX) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(64 * kWaves), 0, stream, p);
-    return hipGetLastError();
 }
 
 // LDS of a workgroup of k_w4_few: scales, and A where it is staged, then the wavefronts' sums over both.
@@ -368,13 +256,6 @@ hipError_t launch_few(const W4Problem& p, int fn, bool xl, int cus, hipStream_t 
     }
 }
 
-template <bool F16>
-hipError_t launch_t(const W4Problem& p, hipStream_t stream) {
-    if (p.M <= 16) return launch_blocks(k_w4_rows_t<F16, 1>, p, 16, 64, stream);
-    if (p.M <= 32) return launch_blocks(k_w4_rows_t<F16, 2>, p, 32, 64, stream);
-    return launch_blocks(k_w4_rows_t<F16, 4>, p, 64, 64, stream);
-}
-
 }  // namespace
 
 bool w4_few_applies(const W4Problem& p, int cus) {
@@ -397,11 +278,6 @@ hipError_t launch_w4_short(const W4Problem& p, bool f16, hipStream_t stream, con
     hipLaunchKernelGGL(f16 ? k_w4_short<true> : k_w4_short<false>, dim3((unsigned)std::min<int64_t>(blocks, 65536)),
                        dim3(256), 0, stream, p);
     return hipGetLastError();
-}
-
-hipError_t launch_w4_rows_t(const W4Problem& p, bool f16, hipStream_t stream, const char*& name) {
-    name = f16 ? "f16_w4_rows_t" : "bf16_w4_rows_t";
-    return f16 ? launch_t<true>(p, stream) : launch_t<false>(p, stream);
 }
 
 }  // namespace gemm

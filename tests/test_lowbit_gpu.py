@@ -149,29 +149,33 @@ def test_w4_product(dtype, tr, shape):
     M, rows, cols = shape
     for i, (group, zeros, out, pad) in enumerate([(32, True, "f32", 0), (64, False, dtype, 3), (128, True, "f32", 8)]):
         check_product(M, rows, cols, dtype, group, zeros, tr, out, 10 + i, pad)
-    short = (rows if tr else cols) < 32
-    kernel = "w4_short" if short else "w4_rows_t" if tr else "w4_few" if M <= 16 else "w4_tile"
+    short = (rows if tr else cols) < 32 or (tr and cols < 32)
+    kernel = "w4_short" if short else "w4_tile_t" if tr else "w4_few" if M <= 16 else "w4_tile"
     assert g.gemm_last_kernel() == f"{dtype}_{kernel}"
 
 
 @pytest.mark.parametrize("dtype", BOTH)
-def test_w4_linear_with_k_split_over_workgroups(dtype):
+@pytest.mark.parametrize("tr", [False, True], ids=["linear", "dgrad"])
+def test_w4_product_with_k_split_over_workgroups(dtype, tr):
     """With the workspace, few tiles of C take K in slices whose sums are added in order: the last slice
     shorter, K odd, every output type and step of the epilogue; with a workspace too small the call runs
     without the split."""
     for M, rows, cols, group, out, epi in [(17, 130, 2051, 32, "f32", {}), (33, 257, 4096, 128, dtype, dict(bias=True)),
                                            (64, 100, 2049, 64, "f32", dict(alpha=0.5, beta=-1.0, bias=True, act="gelu")),
                                            (200, 65, 1900, 32, "f16", dict(act="relu")), (500, 33, 4001, 64, "bf16", {})]:
-        check_product(M, rows, cols, dtype, group, True, False, out, 40, pad=1, workspace="own", **epi)
-        assert g.gemm_last_kernel() == f"{dtype}_w4_tile_splitk", (M, rows, cols)
-    w, _ = make_w4(130, 2051, dtype, 32, False, 3)
-    x = randn(17, 2051, dtype, 4)
-    size = g.w4_workspace_size(w, 17)
-    assert size > 0 and size % (17 * 130 * 4) == 0
+        if tr:                             # (no bias and no activation)
+            rows, cols, epi = cols, rows, {k: v for k, v in epi.items() if k in ("alpha", "beta")}
+        check_product(M, rows, cols, dtype, group, True, tr, out, 40, pad=1, workspace="own", **epi)
+        assert g.gemm_last_kernel() == f"{dtype}_w4_tile{'_t' if tr else ''}_splitk", (M, rows, cols)
+    n, k = 130, 2051
+    w, _ = make_w4(k if tr else n, n if tr else k, dtype, 32, False, 3)
+    x = randn(17, k, dtype, 4)
+    size = g.w4_workspace_size(w, 17, transposed=tr)
+    assert size > 0 and size % (17 * n * 4) == 0
     small = torch.full((size,), 0x3f, dtype=torch.uint8, device="cuda")
-    y = g.w4_linear(x, w, workspace=small[:size - 16])
-    assert g.gemm_last_kernel() == f"{dtype}_w4_tile" and (small == 0x3f).all()
-    check_close(y, *product_reference(x.cpu().double(), g.w4_dequantize(w).cpu().double(), False))
+    y = (g.w4_dgrad if tr else g.w4_linear)(x, w, workspace=small[:size - 16])
+    assert g.gemm_last_kernel() == f"{dtype}_w4_tile{'_t' if tr else ''}" and (small == 0x3f).all()
+    check_close(y, *product_reference(x.cpu().double(), g.w4_dequantize(w).cpu().double(), tr))
 
 
 @pytest.mark.parametrize("epi", [dict(bias=True, act="relu"), dict(bias=True, act="gelu"), dict(alpha=-0.5, beta=2.0),
@@ -183,24 +187,41 @@ def test_w4_linear_epilogue(dtype, out, epi):
         check_product(*shape, dtype, 64, True, False, out, 20, pad=1, **epi)
 
 
+# enough columns for 1, 2, 3 and 4 column blocks a workgroup (4096 columns are one round of 256 CUs), few and many
+# rows, K of one step, of several and of enough for 16 wavefronts a workgroup
+FEW = [(1, 4112, 128), (4, 8208, 257), (5, 4112, 160), (16, 4112, 640), (16, 8208, 128), (9, 8208, 1023), (16, 12304, 96),
+       (12, 12304, 300), (3, 4096, 8192), (16, 1000, 8200), (2, 5000, 11008)]
+
+
+@pytest.mark.parametrize("shape", FEW, ids=str)
+@pytest.mark.parametrize("dtype", BOTH)
+def test_w4_linear_of_few_rows_and_many_columns(dtype, shape):
+    M, rows, cols = shape
+    for group, zeros, out in [(32, True, "f32"), (128, False, dtype)]:
+        check_product(M, rows, cols, dtype, group, zeros, False, out, 50)
+        assert g.gemm_last_kernel() == f"{dtype}_w4_few"
+
+
+# (M, N, K) for which W is written as 16-bit numbers first, with a workspace for them
+MANY = [(2100, 1001, 131), (1100, 2051, 136), (9000, 257, 131)]
+
+
 @pytest.mark.parametrize("tr", [False, True], ids=["linear", "dgrad"])
 @pytest.mark.parametrize("dtype", BOTH)
 def test_w4_product_of_many_rows(dtype, tr):
-    """From the row count on at which W is written as 16-bit numbers first, with and without the
-    workspace; odd extents, so that rows of the workspace are padded."""
-    for M, rows, cols, out, epi in [(600, 130, 200, "f32", {}), (520, 257, 131, dtype, dict(alpha=0.5, beta=1.0)),
-                                    (700, 264, 1030, "f16", {}), (128, 1001, 77, "bf16", dict(beta=-1.0))]:
-        M += 0 if tr else 3968
+    """With and without the workspace; odd extents, so that rows of the workspace are padded."""
+    for (M, n, k), out, epi in zip(MANY, ["f32", dtype, "f16"], [{}, dict(alpha=0.5, beta=1.0), dict(beta=-1.0)]):
+        rows, cols = (k, n) if tr else (n, k)
         check_product(M, rows, cols, dtype, 32, True, tr, out, 30, workspace="own", **epi)
         assert "_dma" in g.gemm_last_kernel()
         check_product(M, rows, cols, dtype, 32, True, tr, out, 30, workspace="none", **epi)
-        assert g.gemm_last_kernel() == f"{dtype}_w4_rows_t" if tr else f"{dtype}_w4_tile"
+        assert g.gemm_last_kernel() == f"{dtype}_w4_tile" + ("_t" if tr else "")
 
 
 @pytest.mark.parametrize("dtype", BOTH)
 def test_w4_linear_of_many_rows_with_bias_and_activation(dtype):
     for act in ("none", "relu", "gelu"):
-        check_product(4100, 300, 264, dtype, 128, False, False, dtype, 31, workspace="own", bias=True, act=act)
+        check_product(2100, 1001, 131, dtype, 128, False, False, dtype, 31, workspace="own", bias=True, act=act)
         assert "_dma" in g.gemm_last_kernel()
 
 
@@ -209,7 +230,7 @@ def test_w4_linear_of_many_rows_with_bias_and_activation(dtype):
 def test_w4_product_is_exact_on_small_integers(dtype, tr):
     """Integers whose sums FP32 holds exactly: every kernel gives the same bits."""
     rng = np.random.default_rng(5)
-    for M, rows, cols in [(1, 70, 300), (40, 33, 640), (600, 130, 136)]:
+    for M, rows, cols in [(1, 70, 300), (40, 33, 640), (600, 130, 136), (1600, 900, 400)]:
         codes = rng.integers(0, 16, (rows, cols)).astype(np.uint8)
         groups = -(-cols // 32)
         s = to_type(2.0 ** rng.integers(-1, 2, (rows, groups)), dtype)
@@ -454,29 +475,33 @@ def test_gradients_against_differences():
 
 
 # ---- streams, graphs, repeats -------------------------------------------------------------------
-def every_call(dtype, rows=600):
+def every_call(dtype, rows=2100):
     """One call of each kind on fixed inputs: (call, outputs it writes)."""
-    w, _ = make_w4(200, 264, dtype, 32, True, 3)
+    w, _ = make_w4(1000, 264, dtype, 32, True, 3)
     weights, x1, xm = randn(40, 130, dtype, 2), randn(1, 264, dtype, 4), randn(rows, 264, dtype, 5)
-    dy = randn(rows, 200, dtype, 6)
+    x64, dy, dy9 = randn(64, 264, dtype, 7), randn(rows, 1000, dtype, 6), randn(9, 1000, dtype, 8)
     f = lambda *s, t=torch.float32: torch.full(s, float("nan"), dtype=t, device="cuda")  # noqa: E731
     q4 = g.w4_quantize(weights, 64, zero_points=True)
     q8 = g.x8_quantize(xm)
     d4, d8 = f(40, 130, t=DTYPES[dtype]), f(rows, 264, t=DTYPES[dtype])
-    y1, ym, dx, dw = f(1, 200), f(rows, 200, t=DTYPES[dtype]), f(rows, 264), f(200, 264)
-    ws = torch.empty(max(g.w4_workspace_size(w, rows), g.w4_workspace_size(w, rows, True),
-                         g.x8_wgrad_workspace_size(q8, 200)), dtype=torch.uint8, device="cuda")
+    y1, y64, ym, dx, dx9 = f(1, 1000), f(64, 1000), f(rows, 1000, t=DTYPES[dtype]), f(rows, 264), f(9, 264)
+    dw = f(1000, 264)
+    # (one workspace for all: they run one after the other)
+    ws = torch.empty(max(*(g.w4_workspace_size(w, m, t) for m in (9, 64, rows) for t in (False, True)),
+                         g.x8_wgrad_workspace_size(q8, 1000)), dtype=torch.uint8, device="cuda")
 
     def call():
         g.w4_quantize(weights, 64, zero_points=True, out=q4)
         g.w4_dequantize(q4, out=d4)
         g.w4_linear(x1, w, out=y1, workspace=ws)
+        g.w4_linear(x64, w, out=y64, workspace=ws)
         g.w4_linear(xm, w, out=ym, workspace=ws)
         g.x8_quantize(xm, out=q8)
         g.x8_dequantize(q8, out=d8)
         g.w4_dgrad(dy, w, out=dx, workspace=ws)
+        g.w4_dgrad(dy9, w, out=dx9, workspace=ws)
         g.x8_wgrad(dy, q8, out=dw, workspace=ws)
-    outs = [q4.codes, q4.scales, q4.zeros, q8.codes, q8.exponents, d4, d8, y1, ym, dx, dw]
+    outs = [q4.codes, q4.scales, q4.zeros, q8.codes, q8.exponents, d4, d8, y1, y64, ym, dx, dx9, dw]
     return call, outs
 
 
