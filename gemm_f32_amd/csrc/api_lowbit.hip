@@ -182,9 +182,39 @@ gemm_status_t w4_product(bool f16, int64_t M, int64_t N, int64_t K, const uint16
 }
 
 // ---- weight gradient from 8-bit activations -----------------------------------------------
+// K (the tokens) split over workgroups where C has too few 256 x 128 tiles to fill the CUs: the number of slices
+// by a time model fitted to 4095 tokens x 1030 x 1023 (40 tiles, fp16): unsplit 55 us, 0.85 us a k-tile of 64
+// tokens; 4 slices 23.6 us (1.3 us a k-tile, the operands' traffic past the L2s among more workgroups) and 5.6 us
+// for the second kernel, which reads the slices' sums at 3 TB/s.  Powers of two: the slices then divide the XCDs.
+struct X8Split {
+    int slices = 1, kslice = 0;
+    size_t bytes = 0;
+};
+
+X8Split x8_split(int64_t T, int64_t N, int64_t K, int cus) {
+    const int64_t tiles = ((N + 255) / 256) * ((K + 127) / 128), steps = (T + 63) / 64;
+    X8Split best;
+    double best_us = 0.85 * steps;
+    for (int64_t s = 2; s <= 32 && s * tiles <= cus && s <= steps; s *= 2) {
+        const int64_t each = (steps + s - 1) / s, used = (steps + each - 1) / each;
+        const double us = 1.3 * each + 2.0 + used * N * K * 4 / 3e6;
+        if (us >= best_us) continue;
+        best_us = us;
+        best = X8Split{(int)used, (int)(64 * each), (size_t)(used * N * K) * 4};
+    }
+    return best;
+}
+
+// Bytes of the 16-bit numbers that the product reads: X, and dY where its rows are not whole chunks of 8.
+size_t x8_decoded(int64_t T, int64_t N, int64_t K) {
+    return (size_t)T * (round8(K) + (N % 8 != 0 ? round8(N) : 0)) * 2;
+}
+
 size_t x8_workspace(int64_t T, int64_t N, int64_t K) {
     if (T <= 0 || N <= 0 || K <= 0) return 0;
-    return (size_t)T * (round8(K) + (N % 8 != 0 ? round8(N) : 0)) * 2;
+    int cus = 0;
+    if (!current_device(cus)) cus = 256;
+    return x8_decoded(T, N, K) + x8_split(T, N, K, cus).bytes;
 }
 
 gemm_status_t x8_wgrad(bool f16, int64_t T, int64_t N, int64_t K, const uint16_t* dY, int64_t lddy, const gemm_x8_t* X,
@@ -211,7 +241,30 @@ gemm_status_t x8_wgrad(bool f16, int64_t T, int64_t N, int64_t K, const uint16_t
     hipError_t err = launch_x8_dequantize(x, (int)T, (int)K, xs, round8(K), f16, stream);
     if (err == hipSuccess && copy) err = launch_copy16(dY, lddy, (int)T, (int)N, ys, round8(N), stream);
     const char* name = "none";
-    if (err == hipSuccess) err = run_fused_tiles(f16 ? In::F16 : In::BF16, p, e, C, cus, stream, name);
+    if (err != hipSuccess) return record_call(err, name);
+    const X8Split sp = x8_split(T, N, K, cus);
+    if (sp.slices > 1) {
+        name = f16 ? "f16_dma256x128_tn_splitk" : "bf16_dma256x128_tn_splitk";
+        float* part = reinterpret_cast<float*>(static_cast<char*>(workspace) + x8_decoded(T, N, K));
+        SplitProblem s{};
+        static_cast<Problem&>(s) = p;
+        s.C = part;
+        s.ldc = p.N;
+        s.kslice = sp.kslice;
+        s.part = part + N * K;
+        Launch l{};
+        l.stream = stream;
+        l.vec_c = p.N % 4 == 0;
+        l.group_m = 1;
+        err = launch_bf16_dma_tn_split(s, sp.slices, l, f16);
+        EpiProblem ep{};
+        static_cast<Problem&>(ep) = p;
+        ep.C = static_cast<float*>(C);
+        ep.e = e;
+        if (err == hipSuccess) err = launch_join_slabs(ep, part, sp.slices, stream);
+    } else {
+        err = run_fused_tiles(f16 ? In::F16 : In::BF16, p, e, C, cus, stream, name);
+    }
     return record_call(err, name);
 }
 

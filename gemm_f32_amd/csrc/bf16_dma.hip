@@ -164,7 +164,9 @@ void k_bf16_dma(typename ModeArgT<MODE>::type p, int tiles_m, int tiles_n, int g
     constexpr int BM = C::BM, BN = C::BN, BK = C::BK, FM = C::FM, FN = C::FN, SUB = C::SUB;
     constexpr int ROW = C::ROW, MF = C::MF;
     __shared__ __align__(16) unsigned char smem[C::LDS];
-    if constexpr (MODE == kSplitK) p.select(blockIdx.y, ES);
+    // slices: grid y, or (ARM) grid x with the tiles along y, so that workgroups of one slice meet on the
+    // XCDs that it is given and each XCD's L2 holds only their k-rows
+    if constexpr (MODE == kSplitK) p.select(ARM ? blockIdx.x : blockIdx.y, ES);
 
     int tm, tn;
     if constexpr (BATCH) {
@@ -174,7 +176,7 @@ void k_bf16_dma(typename ModeArgT<MODE>::type p, int tiles_m, int tiles_n, int g
         tm = __builtin_amdgcn_readfirstlane(tm);
         tn = __builtin_amdgcn_readfirstlane(tn);
     } else {
-        tile_coords(blockIdx.x, tiles_m, tiles_n, group_m, tm, tn);
+        tile_coords(ARM && MODE == kSplitK ? blockIdx.y : blockIdx.x, tiles_m, tiles_n, group_m, tm, tn);
     }
     const int m0 = tm * BM, n0 = tn * BN;
     const bool interior = m0 + BM <= p.M && n0 + BN <= p.N;
@@ -861,19 +863,20 @@ hipError_t launch_bf16_dma_epi(const EpiProblem& p, const Launch& l, int bm, int
 
 // The weight gradient's layout: column-major A and row-major B (ARM), any M and N whose rows of A and
 // columns of B can be read up to the next multiple of 8, any K >= 1 (fewer than 64: the K tail alone).
-template <typename C>
-static hipError_t launch_tn(const EpiProblem& p, const Launch& l, bool f16) {
+template <typename C, int MODE = kEpilogue>
+static hipError_t launch_tn(const typename ModeArgT<MODE>::type& p, const Launch& l, bool f16, int slices = 1) {
     const int tiles_m = (p.M + C::BM - 1) / C::BM, tiles_n = (p.N + C::BN - 1) / C::BN;
     auto go = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, dim3((unsigned)tiles_m * tiles_n), dim3(C::THREADS), 0, l.stream, p, tiles_m,
-                           tiles_n, l.group_m);
+        const unsigned tiles = (unsigned)tiles_m * tiles_n;
+        const dim3 grid = MODE == kSplitK ? dim3((unsigned)slices, tiles) : dim3(tiles);
+        hipLaunchKernelGGL(kernel, grid, dim3(C::THREADS), 0, l.stream, p, tiles_m, tiles_n, l.group_m);
         return hipGetLastError();
     };
     if (f16)
-        return l.vec_c ? go(k_bf16_dma<C, true, kInF16, kEpilogue, false, true, true>)
-                       : go(k_bf16_dma<C, false, kInF16, kEpilogue, false, true, true>);
-    return l.vec_c ? go(k_bf16_dma<C, true, kInBf16, kEpilogue, false, true, true>)
-                   : go(k_bf16_dma<C, false, kInBf16, kEpilogue, false, true, true>);
+        return l.vec_c ? go(k_bf16_dma<C, true, kInF16, MODE, false, true, true>)
+                       : go(k_bf16_dma<C, false, kInF16, MODE, false, true, true>);
+    return l.vec_c ? go(k_bf16_dma<C, true, kInBf16, MODE, false, true, true>)
+                   : go(k_bf16_dma<C, false, kInBf16, MODE, false, true, true>);
 }
 
 bool bf16_dma_tn_applies(const Problem& p) {
@@ -887,6 +890,10 @@ hipError_t launch_bf16_dma_tn(const EpiProblem& p, const Launch& l, int bm, int 
     if (bm == 256 && bn == 256) return launch_tn<Cfg256>(p, l, f16);
     if (bm == 256 && bn == 128) return launch_tn<Cfg<256, 128, 4, 2, 4, 3>>(p, l, f16);
     return hipErrorInvalidValue;
+}
+
+hipError_t launch_bf16_dma_tn_split(const SplitProblem& s, int slices, const Launch& l, bool f16) {
+    return launch_tn<Cfg<256, 128, 4, 2, 4, 3>, kSplitK>(s, l, f16, slices);
 }
 
 // Split-K: s.part holds the slabs of slices 1 .. S-1 (16-byte aligned; l.vec_c also covers their

@@ -425,39 +425,6 @@ __global__ __launch_bounds__(64 * kWavesT, 2) void k_w4_tile_t(W4Problem p, int 
     store_tile<FM>(p, part, vec, acc, reinterpret_cast<float*>(lds) + wave * 32 * kEpRow, m0, n0 + 32 * wave, lane);
 }
 
-// C = epilogue(slab 0 + slab 1 + ...), the slabs dense M x N, added in order: four columns a thread, the
-// slabs' loads four at a time in flight.  vec as for the tile kernel (N % 4 == 0 too).
-__global__ __launch_bounds__(256) void k_w4_join(W4Problem p, const float* part, int slices, int vec) {
-    const int64_t slab = (int64_t)p.M * p.N, groups = (p.N + 3) / 4, total = p.M * groups;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-        const int row = (int)(i / groups), col = 4 * (int)(i - row * groups);
-        const float* src = part + (int64_t)row * p.N + col;
-        const int64_t off = (int64_t)row * p.ldc + col;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f}, old[4] = {0.f, 0.f, 0.f, 0.f}, y[4];
-        if (vec) {
-#pragma unroll 4
-            for (int s = 0; s < slices; ++s) {
-                const float4 v = *reinterpret_cast<const float4*>(src + s * slab);
-                sum[0] += v.x;
-                sum[1] += v.y;
-                sum[2] += v.z;
-                sum[3] += v.w;
-            }
-            if (p.e.beta != 0.f) epi_load4(p.e, p.C, off, old);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = epi_apply(p.e, sum[e], old[e], p.e.bias == nullptr ? 0.f : p.e.bias[col + e]);
-            epi_store4(p.e, p.C, off, y);
-        } else {
-            for (int e = 0; e < 4 && col + e < p.N; ++e) {
-#pragma unroll 4
-                for (int s = 0; s < slices; ++s) sum[e] += src[s * slab + e];
-                if (p.e.beta != 0.f) old[e] = epi_load(p.e, p.C, off + e);
-                epi_store(p.e, p.C, off + e, epi_apply(p.e, sum[e], old[e], p.e.bias == nullptr ? 0.f : p.e.bias[col + e]));
-            }
-        }
-    }
-}
-
 template <bool F16, int FM, int WV, bool TR>
 hipError_t launch_tile(const W4Problem& p, const W4Split& sp, float* part, hipStream_t stream) {
     constexpr int BM = 32 * FM, BN = 32 * WV;
@@ -467,8 +434,8 @@ hipError_t launch_tile(const W4Problem& p, const W4Split& sp, float* part, hipSt
     float* out = sp.slices > 1 ? part : nullptr;
     // 16-byte FP32 or 8-byte 16-bit groups of four columns (the slices' sums start 16-byte aligned)
     const uintptr_t align = p.e.out == kOutF32 ? 16 : 8;
-    const int vec_c = p.ldc % 4 == 0 && reinterpret_cast<uintptr_t>(p.C) % align == 0, vec_n = p.N % 4 == 0;
-    const int vec = out != nullptr ? vec_n : vec_c;
+    const int vec_c = p.ldc % 4 == 0 && reinterpret_cast<uintptr_t>(p.C) % align == 0;
+    const int vec = out != nullptr ? p.N % 4 == 0 : vec_c;
     auto go = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, grid, dim3(64 * WV), 0, stream, p, sp.kslice, out, vec);
         return hipGetLastError();
@@ -488,10 +455,13 @@ hipError_t launch_tile(const W4Problem& p, const W4Split& sp, float* part, hipSt
                   : zp ? go(k_w4_tile<F16, FM, WV, true, false, false>) : go(k_w4_tile<F16, FM, WV, false, false, false>);
     }
     if (err != hipSuccess || sp.slices == 1) return err;
-    const int64_t blocks = ((int64_t)p.M * ((p.N + 3) / 4) + 255) / 256;
-    hipLaunchKernelGGL(k_w4_join, dim3((unsigned)std::min<int64_t>(blocks, 4096)), dim3(256), 0, stream, p, part,
-                       sp.slices, vec_c && vec_n);
-    return hipGetLastError();
+    EpiProblem ep{};
+    ep.M = p.M;
+    ep.N = p.N;
+    ep.C = static_cast<float*>(p.C);
+    ep.ldc = p.ldc;
+    ep.e = p.e;
+    return launch_join_slabs(ep, part, sp.slices, stream);
 }
 
 template <bool F16>

@@ -371,6 +371,30 @@ def test_x8_wgrad(dtype, shape):
         assert torch.equal(buf[:, K:], old[:, K:])
 
 
+@pytest.mark.parametrize("shape", [(257, 300, 200), (1000, 129, 130), (2111, 520, 1030), (4096, 8, 8), (640, 256, 128)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_x8_wgrad_few_tiles(shape):
+    """Tokens split over workgroups: every slice count and last slice, twice the same bits."""
+    T, N, K = shape
+    dy, x = randn(T, N, "bf16", 11), randn(T, K, "bf16", 12)
+    q = g.x8_quantize(x)
+    d, xv = dy.cpu().double(), g.x8_dequantize(q).cpu().double()
+    ws = torch.empty(g.x8_wgrad_workspace_size(q, N), dtype=torch.uint8, device="cuda")
+    for out in ("f32", "bf16", "f16"):
+        buf = torch.randn(N, K + 3, generator=torch.Generator().manual_seed(6)).to(OUTS[out]).cuda()
+        old = buf.clone()
+        ws.fill_(255)
+        say("x8_wgrad few tiles", shape, out)
+        g.x8_wgrad(dy, q, alpha=2.0, beta=0.5, out=buf[:, :K], workspace=ws)
+        ref = 2.0 * (d.t() @ xv) + 0.5 * old[:, :K].cpu().double()
+        size = 2.0 * (d.abs().t() @ xv.abs()) + 0.5 * old[:, :K].cpu().double().abs()
+        check_close(buf[:, :K], ref, sum_bound(T, size))
+        assert torch.equal(buf[:, K:], old[:, K:])
+        again = old.clone()
+        g.x8_wgrad(dy, q, alpha=2.0, beta=0.5, out=again[:, :K])
+        assert torch.equal(again, buf)
+
+
 def test_x8_wgrad_keeps_to_its_columns():
     """A NaN in one token's gradient or activation reaches its row or column of dW only."""
     dy, x = randn(70, 40, "bf16", 1), randn(70, 50, "bf16", 2)
