@@ -20,7 +20,7 @@ int64_t round8(int64_t v) { return (v + 7) / 8 * 8; }
 
 bool extents_ok(int64_t a, int64_t b, int64_t c = 0) {
     for (int64_t v : {a, b, c})
-        if (v < 0 || v > INT_MAX - 255) return false;
+        if (v < 0 || v > INT_MAX - 4095) return false;      // (rounded up to a kernel's block it is still an int)
     return true;
 }
 

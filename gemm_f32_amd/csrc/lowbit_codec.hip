@@ -45,27 +45,56 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
     for (int e = 0; e < 8; ++e) x[e] = from16<F16>((uint16_t)(w[e / 2] >> (16 * (e % 2))));
 }
 
-// whether any of 8 packed numbers is an infinity or a NaN (the exponent field all ones)
-template <bool F16>
-__device__ __forceinline__ bool any_nonfinite(const uint4& v) {
-    constexpr uint32_t E = F16 ? 0x7c00u : 0x7f80u;
-    bool bad = false;
-#pragma unroll
-    for (uint32_t w : {v.x, v.y, v.z, v.w}) bad |= (w & E) == E || ((w >> 16) & E) == E;
-    return bad;
-}
-
 // ---- 4-bit weights -----------------------------------------------------------------------
 // Symmetric (no zeros): s = T(amax / 7), code = round(w / s) + 8.  With zero points: the range always
 // includes 0, s = T((max - min) / 15), z = round(-min / s), code = round(w / s) + z; codes and z are held
 // in 0 .. 15.  s == 0 (a group of zeros, or of numbers too small for a scale of type T): every code is
 // the zero point 8.  A group with an infinity or a NaN gets a NaN scale: all of it stands for NaN.
-// Quotients are correctly rounded divisions: no quotient of two T lies within FP32's rounding of a
-// border between two codes unless it is that border.
-template <bool F16>
+//
+// Roundings are those of correctly rounded divisions, at 3 instructions a quotient: q = a y for y near
+// 1 / b, then q + (a - b q) y, the residual exact.  No quotient of two T lies within FP32's rounding of a border
+// between two codes unless it is that border, and there the second step is exact (all significands of both
+// types and y up to 2 ulp off were tried: 59 million quotients); for b = 7 and 15 it is the correctly rounded
+// quotient of every FP32 significand (tried too).  With the compiler's own divisions and an extreme at a time
+// in FP32 the instructions, not the bytes, set the time: 19.9 us at 4096 x 4096 (bf16, group 128, zero
+// points) and 37.2 at 11008 x 4096 (fp16, symmetric), 3.0 TB/s; so, with extremes of packed 16-bit keys exchanged by
+// lane permutations of the register file, 14.0 (3.1 TB/s) and 22.2 us (5.1 TB/s).
+__device__ __forceinline__ float quotient(float a, float b, float y) {
+    const float q = a * y;
+    return fmaf(fmaf(-q, b, a), y, q);
+}
+
+// d / (7 or 15), correctly rounded (subnormal results and infinity by the plain division)
+template <int B>
+__device__ __forceinline__ float over(float d) {
+    if (!(d >= 0x1p-100f && d < INFINITY)) return d / B;
+    return quotient(d, (float)B, 1.f / B);
+}
+
+// the integer nearest to a q of at most 2^22, ties to even
+__device__ __forceinline__ int nearest(float q) { return (int)(__float_as_uint(q + 0x1.8p23f) - 0x4b400000u); }
+
+typedef short i16x2 __attribute__((ext_vector_type(2)));
+
+// the larger of each half among the 2^k lanes of a group (4, 8 or 16 lanes, all active)
+__device__ __forceinline__ i16x2 group_max(i16x2 v, int lanes) {
+    auto with = [&](auto dpp) {
+        const int o = dpp(__builtin_bit_cast(int, v));
+        v = __builtin_elementwise_max(v, __builtin_bit_cast(i16x2, o));
+    };
+    with([](int u) { return __builtin_amdgcn_mov_dpp(u, 0xb1, 0xf, 0xf, true); });       // lane ^ 1
+    with([](int u) { return __builtin_amdgcn_mov_dpp(u, 0x4e, 0xf, 0xf, true); });       // lane ^ 2
+    if (lanes > 4) with([](int u) { return __builtin_amdgcn_mov_dpp(u, 0x141, 0xf, 0xf, true); });   // 7 - lane
+    if (lanes > 8) with([](int u) { return __builtin_amdgcn_mov_dpp(u, 0x140, 0xf, 0xf, true); });   // 15 - lane
+    return v;
+}
+
+// ZP: with zero points
+template <bool F16, bool ZP>
 __global__ __launch_bounds__(kThreads) void k_w4_quantize(const uint16_t* W, int64_t ldw, int rows, int cols,
                                                           uint8_t* codes, int64_t ld, uint16_t* scales, int64_t lds,
                                                           uint8_t* zeros, int64_t ldz, int gshift) {
+    constexpr short kInf = F16 ? 0x7c00 : 0x7f80;
     const int chunk = blockIdx.x * kThreads + threadIdx.x, c = 8 * chunk;
     const int lanes = 1 << (gshift - 3);          // lanes per group (4, 8 or 16, aligned)
     const bool first = (chunk & (lanes - 1)) == 0 && c < cols;
@@ -78,45 +107,57 @@ __global__ __launch_bounds__(kThreads) void k_w4_quantize(const uint16_t* W, int
         }
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
-            float x[8];
-            unpack8<F16>(v[i], x);
-            float lo = 0.f, hi = 0.f;
+            // Extremes of the bit patterns: magnitudes (no zero points), or keys that order as the numbers do
+            // (negative numbers with the bits below the sign inverted; not-a-numbers beyond the infinities).
+            // top: the largest in its second half, ~ the smallest key in its first.
+            i16x2 most = {0, 0}, least = {0, 0};
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                lo = fminf(lo, x[e]);
-                hi = fmaxf(hi, x[e]);
+            for (uint32_t w : {v[i].x, v[i].y, v[i].z, v[i].w}) {
+                if constexpr (ZP) {
+                    const i16x2 s = __builtin_bit_cast(i16x2, w);
+                    const i16x2 key = s ^ ((s >> 15) & (short)0x7fff);
+                    most = __builtin_elementwise_max(most, key);
+                    least = __builtin_elementwise_min(least, key);
+                } else {
+                    most = __builtin_elementwise_max(most, __builtin_bit_cast(i16x2, w & 0x7fff7fffu));
+                }
             }
-            if (zeros == nullptr) hi = fmaxf(hi, -lo);
-            if (any_nonfinite<F16>(v[i])) hi = INFINITY;
-            for (int d = 1; d < lanes; d *= 2) {
-                hi = fmaxf(hi, __shfl_xor(hi, d));
-                lo = fminf(lo, __shfl_xor(lo, d));
+            const i16x2 top = group_max(i16x2{(short)~min(least.x, least.y), max(most.x, most.y)}, lanes);
+            const bool bad = top.y >= kInf || (ZP && top.x >= kInf);
+            const float hi = from16<F16>((uint16_t)top.y);
+            const float lo = ZP ? -from16<F16>((uint16_t)max(top.x, (short)0)) : 0.f;
+            const uint16_t s16 = bad ? (uint16_t)(F16 ? 0x7e00 : 0x7fc0) : to16<F16>(ZP ? over<15>(hi - lo) : over<7>(hi));
+            float s = from16<F16>(s16), x[8], low = lo;
+            unpack8<F16>(v[i], x);
+            const bool some = s > 0.f && s < INFINITY;
+            if (!F16 && !(s >= 0x1p-100f && s <= 0x1p100f) && some) {
+                // bf16 scales whose reciprocal or residuals could leave FP32's range: all by a power of two
+                const float by = s < 1.f ? 0x1p64f : 0x1p-64f;
+                s *= by;
+                low *= by;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] *= by;
             }
-            const bool bad = hi == INFINITY;
-            const float raw = zeros == nullptr ? hi / 7.f : (hi - lo) / 15.f;
-            const uint16_t s16 = bad ? (uint16_t)(F16 ? 0x7e00 : 0x7fc0) : to16<F16>(raw);
-            const float s = from16<F16>(s16);
-            const bool some = s != 0.f && !bad;
-            const float by = some ? s : 1.f;
-            float z = 8.f;
-            if (zeros != nullptr && some) z = fminf(fmaxf(rintf(-lo / by), 0.f), 15.f);
+            const float y = __builtin_amdgcn_rcpf(s);
+            // (an infinite scale, from a range past FP32: zero point and codes 0, as quotients over it are)
+            int z = 8;
+            if (ZP) z = some ? min(max(nearest(quotient(-low, s, y)), 0), 15) : s == INFINITY ? 0 : 8;
             if (r0 + i >= rows || c >= cols) continue;
             uint32_t w = 0;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float q = some ? rintf(x[e] / by) : 0.f;
-                const uint32_t k = (uint32_t)(int)fminf(fmaxf(q + z, 0.f), 15.f);
-                if (c + e < cols) w |= k << (4 * e);
-            }
+            for (int e = 0; e < 8; ++e)
+                w |= (uint32_t)min(max(nearest(quotient(x[e], s, y)) + z, 0), 15) << (4 * e);
+            if (!some) w = 0x11111111u * (uint32_t)z;
             uint8_t* dst = codes + (r0 + i) * ld + 4 * (int64_t)chunk;
             if (c + 8 <= cols) {
                 *reinterpret_cast<u32_ua*>(dst) = w;
             } else {
+                w &= (1u << (4 * (cols - c))) - 1;       // (the half byte after an odd last column is 0)
                 for (int b = 0; 2 * b < cols - c; ++b) dst[b] = (uint8_t)(w >> (8 * b));
             }
             if (first) {
                 scales[(r0 + i) * lds + (c >> gshift)] = s16;
-                if (zeros != nullptr) zeros[(r0 + i) * ldz + (c >> gshift)] = (uint8_t)z;
+                if (ZP) zeros[(r0 + i) * ldz + (c >> gshift)] = (uint8_t)z;
             }
         }
     }
@@ -270,7 +311,8 @@ hipError_t launch_w4_quantize(const uint16_t* W, int64_t ldw, int rows, int cols
                            const_cast<uint8_t*>(q.zeros), q.ldz, q.gshift);
         return hipGetLastError();
     };
-    return f16 ? go(k_w4_quantize<true>) : go(k_w4_quantize<false>);
+    if (q.zeros != nullptr) return f16 ? go(k_w4_quantize<true, true>) : go(k_w4_quantize<false, true>);
+    return f16 ? go(k_w4_quantize<true, false>) : go(k_w4_quantize<false, false>);
 }
 
 hipError_t launch_w4_dequantize(const W4View& q, int rows, int cols, uint16_t* out, int64_t ldo, bool f16,

@@ -76,6 +76,29 @@ def test_w4_quantize_special_groups(dtype, zeros):
         assert torch.equal(zbuf[:, :2].cpu(), torch.from_numpy(points)) and (zbuf[:, 2:] == 0x5a).all()
 
 
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("dtype", BOTH)
+def test_w4_quantize_every_magnitude(dtype, zeros):
+    """Groups of every power of two that the type has, ties between two codes among their quotients, and a
+    range whose width is past the type's largest number (an infinite scale)."""
+    powers = torch.arange(-133, 127) if dtype == "bf16" else torch.arange(-24, 15)
+    gen = torch.Generator().manual_seed(3)
+    x = torch.randn(len(powers), 64, generator=gen)
+    x[:, 32:] = torch.arange(-16, 16) / 2.0          # scale 8/7 or 1: quotients at borders
+    x[:, 63] = torch.where(torch.arange(len(powers)) % 2 == 0, 7.0, 7.5)
+    w = torch.ldexp(x, powers[:, None] - 3).to(DTYPES[dtype])
+    big = torch.finfo(w.dtype).max
+    w = torch.cat([w, torch.tensor([big, -big] * 32)[None].to(w.dtype)]).cuda()
+    say("w4_quantize magnitudes", dtype, zeros)
+    q = g.w4_quantize(w, 32, zero_points=zeros)
+    with np.errstate(over="ignore"):
+        codes, scales, points = w4_reference(w, 32, zeros, dtype)
+    assert torch.equal(q.scales.cpu().view(torch.int16), scales.view(torch.int16))
+    assert torch.equal(q.codes.cpu(), torch.from_numpy(pack(codes)))
+    if zeros:
+        assert torch.equal(q.zeros.cpu(), torch.from_numpy(points))
+
+
 @pytest.mark.parametrize("dtype", BOTH)
 def test_w4_dequantize_every_code_and_zero_point(dtype):
     """All 16 codes by all 256 zero points, scales of every sign and size (subnormal results among them)."""
