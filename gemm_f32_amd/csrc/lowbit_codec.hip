@@ -3,7 +3,8 @@
 //
 // Every kernel reads its input once and writes its output once, so the time is that of the bytes.
 // A lane owns 8 consecutive columns (16 bytes of the 16-bit side; a wavefront's access to a row is
-// 1 KB contiguous) of kRows rows, all of whose loads are issued before the first is used.  A
+// 1 KB contiguous) of kRows rows, all of whose loads are issued before the first is used (2 rows: rounding 4096 x 4096 to 4 bits 12.3
+// us against 13.4 with 4 and 12.8 with 1, 11008 x 4096 22.4, 21.8 and 26.0).  A
 // group's columns lie in 4 to 16 neighbouring lanes, which agree on its largest magnitude (or its
 // extremes) by exchanging values; one of them writes the scale.
 #include <algorithm>
@@ -15,7 +16,7 @@
 namespace gemm {
 namespace {
 
-constexpr int kThreads = 256, kRows = 4;
+constexpr int kThreads = 256, kRows = 2;
 
 // 8 elements of a row from column c on; zero past cols
 __device__ __forceinline__ uint4 load8(const uint16_t* row, int c, int cols) {
@@ -58,7 +59,7 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
 // quotient of every FP32 significand (tried too).  With the compiler's own divisions and an extreme at a time
 // in FP32 the instructions, not the bytes, set the time: 19.9 us at 4096 x 4096 (bf16, group 128, zero
 // points) and 37.2 at 11008 x 4096 (fp16, symmetric), 3.0 TB/s; so, with extremes of packed 16-bit keys exchanged by
-// lane permutations of the register file, 14.0 (3.1 TB/s) and 22.2 us (5.1 TB/s).
+// lane permutations of the register file, 12.3 (3.4 TB/s) and 22.4 us (5.1 TB/s).
 __device__ __forceinline__ float quotient(float a, float b, float y) {
     const float q = a * y;
     return fmaf(fmaf(-q, b, a), y, q);
