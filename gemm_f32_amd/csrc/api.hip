@@ -818,7 +818,9 @@ hipError_t fused_tiles(In in, const Problem& p, const Epilogue& e, void* C, cons
         l.vec_c = (p.ldc % 4 == 0) && aligned(ep.C, e.out == kOutF32 ? 16 : 8);
         l.group_m = pick_group_m((m + o.bm - 1) / o.bm, (n + o.bn - 1) / o.bn);
         if (f32) return launch_f32_dma_epi(ep, l, o.bm, o.bn);
-        if (tn) return launch_bf16_dma_tn(ep, l, o.bm, o.bn, in == In::F16);
+        if (tn)
+            return identity ? launch_bf16_dma_tn(ep, l, o.bm, o.bn, in == In::F16)
+                            : launch_bf16_dma_tn_epi(ep, l, o.bm, o.bn, in == In::F16);
         return identity ? launch_bf16_dma(ep, l, o.bm, o.bn, in == In::F16)
                         : launch_bf16_dma_epi(ep, l, o.bm, o.bn, in == In::F16);
     };

@@ -238,8 +238,8 @@ gemm_status_t x8_wgrad(bool f16, int64_t T, int64_t N, int64_t K, const uint16_t
     int cus = 0;
     if (!current_device(cus)) return GEMM_ERR_UNSUPPORTED_DEVICE;
     if (T == 0) return record_call(run_epilogue_fill(p, e, C, stream), "epilogue_fill");
-    hipError_t err = launch_x8_dequantize(x, (int)T, (int)K, xs, round8(K), f16, stream);
-    if (err == hipSuccess && copy) err = launch_copy16(dY, lddy, (int)T, (int)N, ys, round8(N), stream);
+    hipError_t err = copy ? launch_x8_operands(x, (int)T, (int)K, xs, round8(K), dY, lddy, (int)N, ys, round8(N), f16, stream)
+                          : launch_x8_dequantize(x, (int)T, (int)K, xs, round8(K), f16, stream);
     const char* name = "none";
     if (err != hipSuccess) return record_call(err, name);
     const X8Split sp = x8_split(T, N, K, cus);

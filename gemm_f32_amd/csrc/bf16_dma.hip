@@ -863,7 +863,7 @@ hipError_t launch_bf16_dma_epi(const EpiProblem& p, const Launch& l, int bm, int
 
 // The weight gradient's layout: column-major A and row-major B (ARM), any M and N whose rows of A and
 // columns of B can be read up to the next multiple of 8, any K >= 1 (fewer than 64: the K tail alone).
-template <typename C, int MODE = kEpilogue>
+template <typename C, int MODE>
 static hipError_t launch_tn(const typename ModeArgT<MODE>::type& p, const Launch& l, bool f16, int slices = 1) {
     const int tiles_m = (p.M + C::BM - 1) / C::BM, tiles_n = (p.N + C::BN - 1) / C::BN;
     auto go = [&](auto kernel) {
@@ -886,9 +886,15 @@ bool bf16_dma_tn_applies(const Problem& p) {
            ((int64_t)(p.K - 1) * p.ldb + p.N + 7) * 2 < lim;
 }
 
-hipError_t launch_bf16_dma_tn(const EpiProblem& p, const Launch& l, int bm, int bn, bool f16) {
-    if (bm == 256 && bn == 256) return launch_tn<Cfg256>(p, l, f16);
-    if (bm == 256 && bn == 128) return launch_tn<Cfg<256, 128, 4, 2, 4, 3>>(p, l, f16);
+hipError_t launch_bf16_dma_tn(const Problem& p, const Launch& l, int bm, int bn, bool f16) {
+    if (bm == 256 && bn == 256) return launch_tn<Cfg256, kPlain>(p, l, f16);
+    if (bm == 256 && bn == 128) return launch_tn<Cfg<256, 128, 4, 2, 4, 3>, kPlain>(p, l, f16);
+    return hipErrorInvalidValue;
+}
+
+hipError_t launch_bf16_dma_tn_epi(const EpiProblem& p, const Launch& l, int bm, int bn, bool f16) {
+    if (bm == 256 && bn == 256) return launch_tn<Cfg256, kEpilogue>(p, l, f16);
+    if (bm == 256 && bn == 128) return launch_tn<Cfg<256, 128, 4, 2, 4, 3>, kEpilogue>(p, l, f16);
     return hipErrorInvalidValue;
 }
 

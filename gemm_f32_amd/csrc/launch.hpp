@@ -89,9 +89,10 @@ hipError_t launch_zero_c(const Problem& p, const Launch& l);
 hipError_t launch_bf16_dma_epi(const EpiProblem& p, const Launch& l, int bm, int bn, bool f16);
 hipError_t launch_epi_fill(const EpiProblem& p, const Launch& l);
 // The 16-bit direct-copy kernel on a column-major A and a row-major B (a weight gradient's layout), with
-// the epilogue: any K >= 1; rows of A and columns of B must be readable up to the next multiple of 8.
+// or without the epilogue: any K >= 1; rows of A and columns of B must be readable up to the next multiple of 8.
 bool bf16_dma_tn_applies(const Problem& p);
-hipError_t launch_bf16_dma_tn(const EpiProblem& p, const Launch& l, int bm, int bn, bool f16);
+hipError_t launch_bf16_dma_tn(const Problem& p, const Launch& l, int bm, int bn, bool f16);
+hipError_t launch_bf16_dma_tn_epi(const EpiProblem& p, const Launch& l, int bm, int bn, bool f16);
 // The same with K split: 256 x 128 tiles, every slice's sums (s.kslice deep, a multiple of 64) into a dense
 // M x N slab of s.C, s.part the second slab; launch_join_slabs follows.
 hipError_t launch_bf16_dma_tn_split(const SplitProblem& s, int slices, const Launch& l, bool f16);

@@ -57,8 +57,8 @@ hipError_t launch_x8_quantize(const uint16_t* X, int64_t ldx, int rows, int cols
 hipError_t launch_x8_dequantize(const X8View& q, int rows, int cols, uint16_t* out, int64_t ldo, bool f16,
                                 hipStream_t stream);
 // rows x cols 16-bit elements into rows of ldo elements
-hipError_t launch_copy16(const uint16_t* in, int64_t ldi, int rows, int cols, uint16_t* out, int64_t ldo,
-                         hipStream_t stream);
+hipError_t launch_x8_operands(const X8View& q, int rows, int cols, uint16_t* out, int64_t ldo, const uint16_t* dy,
+                              int64_t lddy, int n, uint16_t* dy_out, int64_t ld_dy_out, bool f16, hipStream_t stream);
 // The products (w4_rows.hip, w4_tile.hip); each sets the name that gemm_last_kernel() reports.
 // Fewer than 32 k (or, dy . W, 32 columns): any M, N, either order.
 hipError_t launch_w4_short(const W4Problem& p, bool f16, hipStream_t stream, const char*& name);

@@ -257,8 +257,7 @@ __global__ __launch_bounds__(kThreads) void k_x8_quantize(const uint16_t* X, int
 }
 
 template <bool F16>
-__global__ __launch_bounds__(kThreads) void k_x8_dequantize(X8View q, int rows, int cols, uint16_t* out,
-                                                            int64_t ldo) {
+__device__ __forceinline__ void x8_dequantize_rows(const X8View& q, int rows, int cols, uint16_t* out, int64_t ldo) {
     const int chunk = blockIdx.x * kThreads + threadIdx.x, c = 8 * chunk;
     if (c >= cols) return;
     for (int64_t r0 = (int64_t)blockIdx.y * kRows; r0 < rows; r0 += (int64_t)gridDim.y * kRows) {
@@ -289,11 +288,31 @@ __global__ __launch_bounds__(kThreads) void k_x8_dequantize(X8View q, int rows, 
     }
 }
 
-__global__ __launch_bounds__(kThreads) void k_copy16(const uint16_t* in, int64_t ldi, int rows, int cols,
-                                                     uint16_t* out, int64_t ldo) {
+template <bool F16>
+__global__ __launch_bounds__(kThreads) void k_x8_dequantize(X8View q, int rows, int cols, uint16_t* out, int64_t ldo) {
+    x8_dequantize_rows<F16>(q, rows, cols, out, ldo);
+}
+
+// The 16-bit operands of a weight gradient in one launch: X's numbers (grid z = 0), and dY in rows of whole
+// chunks of 8 (z = 1; its columns past the end are left as they are, and give rows of C that do not exist).
+template <bool F16>
+__global__ __launch_bounds__(kThreads) void k_x8_operands(X8View q, int rows, int cols, uint16_t* out, int64_t ldo,
+                                                          const uint16_t* dy, int64_t lddy, int n, uint16_t* dy_out,
+                                                          int64_t ld_dy_out) {
+    if (blockIdx.z == 0) {
+        x8_dequantize_rows<F16>(q, rows, cols, out, ldo);
+        return;
+    }
     const int c = 8 * (blockIdx.x * kThreads + threadIdx.x);
-    if (c >= cols) return;
-    for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) store8(out + r * ldo, c, cols, load8(in + r * ldi, c, cols));
+    if (c >= n) return;
+    for (int64_t r0 = (int64_t)blockIdx.y * kRows; r0 < rows; r0 += (int64_t)gridDim.y * kRows) {
+        uint4 v[kRows];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) v[i] = load8(dy + min(r0 + i, (int64_t)rows - 1) * lddy, c, n);
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+            if (r0 + i < rows) store8(dy_out + (r0 + i) * ld_dy_out, c, n, v[i]);
+    }
 }
 
 // a grid of 256 x 8 columns by `per` rows (65535 row blocks at most; the kernels stride over the rest)
@@ -344,10 +363,15 @@ hipError_t launch_x8_dequantize(const X8View& q, int rows, int cols, uint16_t* o
     return f16 ? go(k_x8_dequantize<true>) : go(k_x8_dequantize<false>);
 }
 
-hipError_t launch_copy16(const uint16_t* in, int64_t ldi, int rows, int cols, uint16_t* out, int64_t ldo,
-                         hipStream_t stream) {
-    hipLaunchKernelGGL(k_copy16, grid_for(rows, cols, 1), dim3(kThreads), 0, stream, in, ldi, rows, cols, out, ldo);
-    return hipGetLastError();
+hipError_t launch_x8_operands(const X8View& q, int rows, int cols, uint16_t* out, int64_t ldo, const uint16_t* dy,
+                              int64_t lddy, int n, uint16_t* dy_out, int64_t ld_dy_out, bool f16, hipStream_t stream) {
+    dim3 grid = grid_for(rows, std::max(cols, n), kRows);
+    grid.z = 2;
+    auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, q, rows, cols, out, ldo, dy, lddy, n, dy_out, ld_dy_out);
+        return hipGetLastError();
+    };
+    return f16 ? go(k_x8_operands<true>) : go(k_x8_operands<false>);
 }
 
 }  // namespace gemm
