@@ -450,7 +450,7 @@ typedef struct {
  * each held in 0 .. 15, rounding to nearest with ties to even, divisions in FP32.  A scale of 0 gives
  * codes and zero point 8; a group with an infinity or a NaN gets a NaN scale.
  * gemm_bf16_w4_dequantize / gemm_f16_w4_dequantize: writes the matrix Q stands for.
- * Errors: GEMM_ERR_INVALID_VALUE for negative or too large extents (> INT_MAX), a leading dimension
+ * Errors: GEMM_ERR_INVALID_VALUE for negative or too large extents (> 2^31 - 4096), a leading dimension
  * too small, an unknown group, a null pointer for a non-empty matrix, or a 16-bit pointer at an odd
  * address; GEMM_ERR_UNSUPPORTED_DEVICE and GEMM_ERR_LAUNCH as for the products. */
 gemm_status_t gemm_bf16_w4_quantize(int64_t rows, int64_t cols, const uint16_t *W, int64_t ldw,
@@ -467,12 +467,14 @@ gemm_status_t gemm_f16_w4_dequantize(int64_t rows, int64_t cols, const gemm_w4_t
  * for either T).  epilogue == NULL: C = A.B in FP32.  B is K x N:
  *   order_b == GEMM_COL_MAJOR  W holds B^T, N rows of K columns: a layer's forward product x . W^T
  *   order_b == GEMM_ROW_MAJOR  W holds B, K rows of N columns: the layer's input gradient dy . W
- * Any M, N, K and alignment; K == 0 gives act(beta * C + bias).  Few rows are decoded inside the
- * product; for many, W is first written as T into the workspace, from which the 16-bit direct-copy
- * kernels run (gemm_last_kernel() names them).  Results are deterministic.
- * workspace: device memory, 16-byte aligned, not overlapping A, C or W, used only if workspace_bytes >=
- * gemm_w4_workspace_size(...) and that is not 0; without it every problem runs on the kernel for few
- * rows.  Calls that share one workspace must not run concurrently.
+ * Any M, N, K and alignment; K == 0 gives act(beta * C + bias).  W is decoded inside the product, or,
+ * for many rows where that is the faster way, first written as T into the workspace, from which the
+ * 16-bit direct-copy kernels run (gemm_last_kernel() names what ran).  Results are deterministic.
+ * workspace: device memory, 16-byte aligned, not overlapping A, C or W, of gemm_w4_workspace_size(...)
+ * bytes (of the current device; 0: the call uses none) for W's 16-bit numbers or, where K is divided
+ * among workgroups, their FP32 sums.  With less, or NULL, the product runs without either: the same
+ * result but for the order of its sums, and slower.  Calls that share one workspace must not run
+ * concurrently.
  * Errors: GEMM_ERR_INVALID_VALUE as for the other products and gemm_w4_quantize, and for an unknown order,
  * activation or output type, a bias not 4-byte aligned, a C not aligned to its element, or a workspace
  * not 16-byte aligned. */
@@ -513,8 +515,9 @@ typedef struct {
  * 16-bit per out_type): dY is T x N tokens by output features, row-major, type T, X is T x K in 8 bits.
  * Products and sums are FP32; beta = 1 adds to the gradient of earlier micro-batches.
  * workspace: device memory, 16-byte aligned, of at least gemm_x8_wgrad_workspace_size(tokens, N, K)
- * bytes, not overlapping the other operands: X's 16-bit numbers, and dY where N % 8 != 0.  Calls that
- * share one must not run concurrently.  tokens == 0 gives beta * C.
+ * bytes (of the current device), not overlapping the other operands: X's 16-bit numbers, dY where
+ * N % 8 != 0, and the FP32 sums of tokens divided among workgroups.  Calls that share one must not run
+ * concurrently.  Results are deterministic.  tokens == 0 gives beta * C.
  * Errors: as for the 4-bit calls, and GEMM_ERR_INVALID_VALUE for a workspace that is missing or too
  * small, and for operands whose element offsets reach 2^30 (tokens * N, tokens * K with the leading
  * dimension of dY). */
