@@ -1,18 +1,18 @@
-// Few rows times a 4-bit matrix: C = epilogue(A . B), A 16-bit row-major, B in 4-bit codes with a scale
-// per group of columns (lowbit.hpp), decoded in registers on the way to the matrix instructions.
+// At most 16 rows times a 4-bit matrix, x . W^T, and the products too short for any matrix instruction:
+// C = epilogue(A . B), A 16-bit row-major, B stored N x K in 4-bit codes with a scale per group of columns
+// (lowbit.hpp), decoded in registers on the way to the matrix instructions.
 //
-// With few rows the product is bound by reading B, a quarter of the bytes of a 16-bit B, so B goes
-// from memory straight to the lane that decodes it, and each code is read and decoded once per
-// 16 FM rows.  Two orders of B:
-//  * TR = false, B stored N x K (x . W^T): lane l of a 16 x 16 x 32 matrix instruction supplies
-//    column l % 16 with 8 consecutive k.  It loads the 16 bytes of 32 consecutive codes, one group's
-//    (groups are 32 or more, aligned), which are the operands of four instructions: a wavefront's
-//    load is 64 contiguous bytes of each of 16 rows of W.
-//  * TR = true, B stored K x N (dy . W): k runs over the rows of W.  Lane l loads two bytes, columns
-//    4 (l % 16) .. + 3, of each of the 8 rows 8 (l / 16) ..: code j of each is the operand of
-//    instruction j, which computes columns 4 i + j.  No transposition in LDS.
-// The workgroup's 8 wavefronts take k in turn and add their sums through LDS in a fixed order
-// (deterministic; no workspace).
+// With few rows the product is bound by reading W, a quarter of the bytes of a 16-bit W, so the codes go
+// from memory straight to the lane that decodes them, each once: lane l of a 16 x 16 x 32 matrix
+// instruction supplies column l % 16 with 8 consecutive k; it loads the 16 bytes of 32 consecutive codes, one
+// group's (groups are 32 or more, aligned), the operands of four instructions, and a wavefront's load is 64
+// contiguous bytes of each of 16 rows of W.  The workgroup's wavefronts take k in turn and add their sums
+// through LDS in a fixed order (deterministic; no workspace).
+//
+// 1 x 4096 x 4096 (bf16): 5.1 us, 1.7 TB/s of W; of them 1.5 are an empty launch, and reading these 8.6 MB at
+// the rate of a large copy would take 1.8.  16 x 11008 x 4096 (fp16): 10.7 to 12.6 us, 2.2 TB/s; a step's loads of A
+// from L2 (as many as W's at three column blocks) and decoding are what it waits for.  Rows of A at odd multiples
+// of 2 bytes cost the loads of A twice their time: 16 x 4096 x 4096 7.8 us, x 4095 16.2.
 #include <algorithm>
 
 #include "common.hpp"
@@ -31,8 +31,8 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 // instructions a CU can issue: so W's codes are all that the loop loads when it can be.
 //  * A workgroup owns 16 FN columns; its NW wavefronts take steps of 128 k in turn.  Latency is hidden by
 //    the other wavefronts of the CU, not by loading further ahead: two or four steps in flight per
-//    wavefront were slower everywhere (1 x 4096 x 4096 4.5 -> 4.9 and 5.2 us, 1 x 11008 x 4096 7.7 -> 8.7
-//    and 9.5, 16 x 11008 x 4096 10.8 -> 12.8), as all of a CU's data then arrives before any is decoded.
+//    wavefront were slower everywhere (1 x 4096 x 4096 by 0.4 and 0.7 us, 1 x 11008 x 4096 by 1.0 and 1.8,
+//    16 x 11008 x 4096 by 2.0), as all of a CU's data then arrives before any is decoded.
 //  * Scales and zero points of the workgroup's columns are staged in LDS first, one word a group, while
 //    the first codes are on their way (two scattered loads a step otherwise).
 //  * XL: so is A, where it is small (a load of A from L2 carries 16 bytes for each of 16 rows, whether
@@ -218,9 +218,9 @@ int64_t few_lds(const W4Problem& p, int fn, int nw, bool xl) {
 }
 
 // Column blocks of 16 per workgroup.  With A in LDS one: more workgroups a CU, some of which load while
-// others decode (1 x 11008 x 4096: 7.7 us against 9.4 and 9.1 with two and three).  Else the fewest columns
-// on the busiest CU, then the widest, since every workgroup reads A (16 x 11008 x 4096: three 10.8 us, one
-// 16.4, two 15.0; 16 x 4096 x 4096: one 7.7, two 9.2).  0: the staged operands do not fit.
+// others decode (1 x 11008 x 4096: 8.7 us; two and three were 1.7 and 1.4 slower).  Else the fewest columns
+// on the busiest CU, then the widest, since every workgroup reads A (16 x 11008 x 4096: three 10.7 us, one
+// 16.4, two 15.0; 16 x 4096 x 4096: one 7.8, two 9.2).  0: the staged operands do not fit.
 bool few_in_lds(const W4Problem& p) { return p.M <= 4 && few_lds(p, 1, 16, true) <= kFewLds; }
 
 int few_blocks(const W4Problem& p, int cus, bool xl) {

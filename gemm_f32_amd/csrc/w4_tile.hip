@@ -481,9 +481,9 @@ hipError_t launch_type(const W4Problem& p, const W4Split& sp, float* part, hipSt
 // takes a workgroup alone on its CU `alone` us, up to `busy` where every CU has one (the power limit lowers the
 // clock), and n workgroups that share a CU n `shared` together.  A split adds a second kernel (4 us) and
 // the slices' sums, written and read once each at 3 TB/s.  Best and second-best measured, x . W^T: 64 x 4096 x
-// 4096 15.1 us (32 x 128 tiles, 4 slices) and 17.3 (64 x 128, 8 slices), unsplit 25.2; 512 x 4096 x 4096 33.9
-// (64 x 128) and 36.4 (128 x 256, 4 slices); 512 x 11008 x 4096 62.1 (128 x 256) and 75.6 (64 x 128); dy . W:
-// 128 x 4096 x 4096 23.7 (64 x 128, 4 slices) and 25.0 (32 x 128, 4 slices), unsplit 37.2.
+// 4096 15.6 us (32 x 128 tiles, 4 slices) and 17.3 (64 x 128, 8 slices), unsplit 25.2; 512 x 4096 x 4096 32.1
+// (64 x 128) and 36.4 (128 x 256, 4 slices); 512 x 11008 x 4096 62.9 (128 x 256) and 75.6 (64 x 128); dy . W:
+// 128 x 4096 x 4096 22.2 (64 x 128, 4 slices) and 25.0 (32 x 128, 4 slices), unsplit 37.2.
 struct TileTime {
     int fm, wv;
     double alone, busy, shared;
