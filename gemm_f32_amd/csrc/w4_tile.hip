@@ -110,7 +110,9 @@ __global__ __launch_bounds__(64 * WV, 2) void k_w4_tile(W4Problem p, int kslice,
     constexpr int BM = 32 * FM, BN = 32 * WV, ROW = 2 * kStep, T = 64 * WV;     // ROW: LDS row bytes
     constexpr int EP = kEpRow;                                               // epilogue: floats per staged row
     constexpr int XBYTES = BM * ROW, EBYTES = WV * 32 * EP * 4, NG = G32 ? 2 : 1;
-    constexpr int COPIES = BM / 4 / WV, LOADS = COPIES + 2 + NG * (ZP ? 2 : 1);    // of a wavefront and step
+    // of a wavefront and step, copies into LDS and the loads that at least follow the step before's copies (the
+    // codes'; the compiler makes one load of a lane's two scales or zero points)
+    constexpr int COPIES = BM / 4 / WV, LOADS = COPIES + 2;
     static_assert(COPIES >= 1 && BM % (4 * WV) == 0, "whole copies per wavefront");
     __shared__ __align__(16) unsigned char lds[kRing * XBYTES > EBYTES ? kRing * XBYTES : EBYTES];
 
@@ -152,14 +154,14 @@ __global__ __launch_bounds__(64 * WV, 2) void k_w4_tile(W4Problem p, int kslice,
     auto load = [&](int b, int k0) {                    // a step wholly inside K
         const int k = k0 + 64 * h;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const u32x4_ub v = *reinterpret_cast<const u32x4_ub*>(crow + k / 2 + 16 * j);
-            c[b][j] = make_uint4(v.x, v.y, v.z, v.w);
-        }
-#pragma unroll
         for (int j = 0; j < NG; ++j) {
             s[b][j] = srow[(k >> gs) + j];
             if constexpr (ZP) z[b][j] = zrow[(k >> gs) + j];
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const u32x4_ub v = *reinterpret_cast<const u32x4_ub*>(crow + k / 2 + 16 * j);
+            c[b][j] = make_uint4(v.x, v.y, v.z, v.w);
         }
 #pragma unroll
         for (int i = 0; i < COPIES; ++i) {
@@ -213,8 +215,8 @@ __global__ __launch_bounds__(64 * WV, 2) void k_w4_tile(W4Problem p, int kslice,
         }
     };
 
-    // Whole steps.  At the barrier of step i every wavefront has waited for its own copies of step i (those of
-    // step i + 1 may be in flight) and is done with step i - 1, whose stage then takes step i + 2.  Past the
+    // Whole steps.  At the barrier of step i every wavefront has waited for its own copies of step i (all but the
+    // LOADS newest loads are then there, and step i + 1 has issued at least as many) and is done with step i - 1, whose stage then takes step i + 2.  Past the
     // last step the last is loaded again, into a stage that nobody reads: no branch.
     const int whole = FAR ? 0 : (K - k_begin) / kStep;
     if (!FAR && whole > 0) {                            // uniform
