@@ -184,7 +184,7 @@ gemm_status_t w4_product(bool f16, int64_t M, int64_t N, int64_t K, const uint16
 // ---- weight gradient from 8-bit activations -----------------------------------------------
 // K (the tokens) split over workgroups where C has too few 256 x 128 tiles to fill the CUs: the number of slices
 // by a time model fitted to 4095 tokens x 1030 x 1023 (40 tiles, fp16): unsplit 55 us, 0.85 us a k-tile of 64
-// tokens; 4 slices 23.6 us (1.3 us a k-tile, the operands' traffic past the L2s among more workgroups) and 5.6 us
+// tokens; 4 slices 21.0 us (1.2 us a k-tile, the operands' traffic past the L2s among more workgroups) and 6.0 us
 // for the second kernel, which reads the slices' sums at 3 TB/s.  Powers of two: the slices then divide the XCDs.
 struct X8Split {
     int slices = 1, kslice = 0;
@@ -197,10 +197,10 @@ X8Split x8_split(int64_t T, int64_t N, int64_t K, int cus) {
     double best_us = 0.85 * steps;
     for (int64_t s = 2; s <= 32 && s * tiles <= cus && s <= steps; s *= 2) {
         const int64_t each = (steps + s - 1) / s, used = (steps + each - 1) / each;
-        const double us = 1.3 * each + 2.0 + used * N * K * 4 / 3e6;
+        const double us = 1.2 * each + 2.0 + used * N * K * 4 / 3e6;
         if (us >= best_us) continue;
         best_us = us;
-        best = X8Split{(int)used, (int)(64 * each), (size_t)(used * N * K) * 4};
+        best = X8Split{(int)used, (int)(64 * each), (size_t)(used * N * ((K + 3) & ~3)) * 4};
     }
     return best;
 }
@@ -248,20 +248,22 @@ gemm_status_t x8_wgrad(bool f16, int64_t T, int64_t N, int64_t K, const uint16_t
         float* part = reinterpret_cast<float*>(static_cast<char*>(workspace) + x8_decoded(T, N, K));
         SplitProblem s{};
         static_cast<Problem&>(s) = p;
+        // sums in rows of whole 16 bytes (the columns past K come from the padding of X's rows and are not read)
+        s.N = (p.N + 3) & ~3;
         s.C = part;
-        s.ldc = p.N;
+        s.ldc = s.N;
         s.kslice = sp.kslice;
-        s.part = part + N * K;
+        s.part = part + N * s.N;
         Launch l{};
         l.stream = stream;
-        l.vec_c = p.N % 4 == 0;
+        l.vec_c = true;
         l.group_m = 1;
         err = launch_bf16_dma_tn_split(s, sp.slices, l, f16);
         EpiProblem ep{};
         static_cast<Problem&>(ep) = p;
         ep.C = static_cast<float*>(C);
         ep.e = e;
-        if (err == hipSuccess) err = launch_join_slabs(ep, part, sp.slices, stream);
+        if (err == hipSuccess) err = launch_join_slabs(ep, part, sp.slices, s.N, stream);
     } else {
         err = run_fused_tiles(f16 ? In::F16 : In::BF16, p, e, C, cus, stream, name);
     }

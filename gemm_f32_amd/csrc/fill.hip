@@ -65,17 +65,17 @@ __global__ __launch_bounds__(256) void k_add_slabs(float* C, int64_t ldc, int M,
     }
 }
 
-// C = epilogue(slab 0 + slab 1 + ...), the slabs dense M x N, added in order: four columns a thread where
+// C = epilogue(slab 0 + slab 1 + ...), the slabs M rows of ldp >= N, added in order: four columns a thread where
 // VEC (N % 4 == 0, 16-byte FP32 or 8-byte 16-bit groups of four columns in C), else one; the slabs' loads four
 // at a time in flight.
 template <bool VEC>
-__global__ __launch_bounds__(256) void k_join_slabs(EpiProblem p, const float* part, int slices) {
+__global__ __launch_bounds__(256) void k_join_slabs(EpiProblem p, const float* part, int slices, int ldp) {
     constexpr int E = VEC ? 4 : 1;
-    const int64_t slab = (int64_t)p.M * p.N, total = slab / E;
+    const int64_t slab = (int64_t)p.M * ldp, total = (int64_t)p.M * p.N / E;
     const int groups = p.N / E;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
         const int row = (int)(i / groups), col = E * (int)(i - (int64_t)row * groups);
-        const float* src = part + i * E;
+        const float* src = part + (int64_t)row * ldp + col;
         const int64_t off = (int64_t)row * p.ldc + col;
         float sum[4] = {0.f, 0.f, 0.f, 0.f}, old[4] = {0.f, 0.f, 0.f, 0.f}, y[4];
 #pragma unroll 4
@@ -113,13 +113,13 @@ hipError_t launch_add_slabs(float* C, int64_t ldc, int M, int N, const float* pa
     return hipGetLastError();
 }
 
-hipError_t launch_join_slabs(const EpiProblem& p, const float* part, int slices, hipStream_t stream) {
+hipError_t launch_join_slabs(const EpiProblem& p, const float* part, int slices, int ldp, hipStream_t stream) {
     const uintptr_t align = p.e.out == kOutF32 ? 16 : 8;
-    const bool vec = p.N % 4 == 0 && p.ldc % 4 == 0 && reinterpret_cast<uintptr_t>(p.C) % align == 0;
+    const bool vec = p.N % 4 == 0 && ldp % 4 == 0 && p.ldc % 4 == 0 && reinterpret_cast<uintptr_t>(p.C) % align == 0;
     const int64_t blocks = std::min<int64_t>(((int64_t)p.M * p.N / (vec ? 4 : 1) + 255) / 256, 8192);
     const dim3 grid((unsigned)blocks), block(256);
-    if (vec) hipLaunchKernelGGL(k_join_slabs<true>, grid, block, 0, stream, p, part, slices);
-    else hipLaunchKernelGGL(k_join_slabs<false>, grid, block, 0, stream, p, part, slices);
+    if (vec) hipLaunchKernelGGL(k_join_slabs<true>, grid, block, 0, stream, p, part, slices, ldp);
+    else hipLaunchKernelGGL(k_join_slabs<false>, grid, block, 0, stream, p, part, slices, ldp);
     return hipGetLastError();
 }
 

@@ -96,8 +96,8 @@ hipError_t launch_bf16_dma_tn_epi(const EpiProblem& p, const Launch& l, int bm, 
 // The same with K split: 256 x 128 tiles, every slice's sums (s.kslice deep, a multiple of 64) into a dense
 // M x N slab of s.C, s.part the second slab; launch_join_slabs follows.
 hipError_t launch_bf16_dma_tn_split(const SplitProblem& s, int slices, const Launch& l, bool f16);
-// C = epilogue(slab 0 + slab 1 + ...), the dense M x N slabs at part added in order (fill.hip)
-hipError_t launch_join_slabs(const EpiProblem& p, const float* part, int slices, hipStream_t stream);
+// C = epilogue(slab 0 + slab 1 + ...), the slabs at part (M rows of ldp floats each) added in order (fill.hip)
+hipError_t launch_join_slabs(const EpiProblem& p, const float* part, int slices, int ldp, hipStream_t stream);
 // Split-K on the 16-bit direct-copy kernel (same requirements as launch_bf16_dma, every slice
 // K >= 64): `slices` K slices of s.kslice as a second grid dimension, slices 1 .. S-1 into the
 // slabs at s.part, then launch_add_slabs (fill.hip) adds them to C in slice order.

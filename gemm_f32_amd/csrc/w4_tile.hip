@@ -463,7 +463,7 @@ hipError_t launch_tile(const W4Problem& p, const W4Split& sp, float* part, hipSt
     ep.C = static_cast<float*>(p.C);
     ep.ldc = p.ldc;
     ep.e = p.e;
-    return launch_join_slabs(ep, part, sp.slices, stream);
+    return launch_join_slabs(ep, part, sp.slices, p.N, stream);
 }
 
 template <bool F16>
